@@ -1,0 +1,207 @@
+// The cache handle: validation, rotation table, tensor maps, status word, and
+// the C entry points of the operators that work on it (include/mk.h).
+#include <math.h>
+#include <string.h>
+
+#include <new>
+
+#include "mk_cache.h"
+
+namespace mk {
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// 2-D map (head_dim columns, all rows) of a cache or pool: boxes of 64 columns
+// x box_rows rows, 128-byte swizzle (16-byte chunk c of row r at c ^ (r & 7)).
+cudaError_t encode_map(const void* base, int64_t rows, int hd, int box_rows, CUtensorMap* out) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)hd * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  const CUresult r = reinterpret_cast<EncodeTiledFn>(p)(
+      out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, elem,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// (cos, sin) of pos * theta^(-2i/hd), angles and functions in double: an angle
+// of a far position has no fraction left in fp32.
+__global__ void rope_table(float2* out, int T, int half, double theta) {
+  const int64_t n = (int64_t)T * half;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+    const int pos = (int)(e / half), i = (int)(e % half);
+    double s, c;
+    sincos((double)pos * pow(theta, -(double)i / half), &s, &c);
+    out[e] = make_float2((float)c, (float)s);
+  }
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// The handle's device must be the current one: its pointers and the caller's stream belong to it.
+int on_device(const mk_cache* c) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MK_ERR_CUDA;
+  return dev == c->device ? MK_OK : MK_ERR_INVALID_ARG;
+}
+
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return MK_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mk
+
+extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_cache** out) {
+  if (!out) return MK_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!desc || !kv || !kv->k || !kv->v) return MK_ERR_INVALID_ARG;
+  const mk_cache_desc& d = *desc;
+  if (d.n_layers <= 0 || d.batch <= 0 || d.n_q_heads <= 0 || d.n_kv_heads <= 0 || d.head_dim <= 0 || d.max_ctx <= 0 ||
+      !(d.rms_eps >= 0) || !(d.rope_theta > 0))
+    return MK_ERR_INVALID_ARG;
+  if (kv->block_table && (kv->page_size <= 0 || kv->n_pages <= 0)) return MK_ERR_INVALID_ARG;
+  if ((d.head_dim != 64 && d.head_dim != 128) || d.n_q_heads % d.n_kv_heads ||
+      d.n_q_heads / d.n_kv_heads > mk::kCacheMaxGroup || d.batch > mk::kCacheMaxBatch ||
+      !mk::aligned(kv->k, 16) || !mk::aligned(kv->v, 16) || !mk::aligned(kv->block_table, 4) ||
+      (kv->block_table && kv->page_size % mk::kCachePageUnit) || d.max_ctx > (1 << 30) || d.n_q_heads > (1 << 16))
+    return MK_ERR_UNSUPPORTED;
+  // rows of the cache, each factor below 2^31: compare step by step
+  const int64_t limit = (int64_t)1 << 31;
+  const int64_t factors[4] = {d.n_layers, kv->block_table ? kv->n_pages : d.batch, d.n_kv_heads,
+                              kv->block_table ? kv->page_size : d.max_ctx};
+  int64_t rows = 1;
+  for (int64_t f : factors) {
+    rows *= f;
+    if (rows >= limit) return MK_ERR_UNSUPPORTED;
+  }
+
+  int dev = 0, n_sm = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  if (major != 10 || minor != 0) return MK_ERR_UNSUPPORTED;
+  if (mk::attend_prepare() != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  mk_cache* c = new (std::nothrow) mk_cache();
+  if (!c) return MK_ERR_CUDA;
+  c->d = d;
+  c->device = dev;
+  c->n_sm = n_sm;
+  c->k = (uint16_t*)kv->k;
+  c->v = (uint16_t*)kv->v;
+  c->box = mk::cache_box_rows(kv->block_table ? kv->page_size : 0);
+  cudaError_t e = mk::encode_map(kv->k, rows, d.head_dim, c->box, &c->kmap);
+  if (e == cudaSuccess) e = mk::encode_map(kv->v, rows, d.head_dim, c->box, &c->vmap);
+  if (e != cudaSuccess) {
+    delete c;
+    return e == cudaErrorInvalidValue ? MK_ERR_UNSUPPORTED : MK_ERR_CUDA;
+  }
+  const size_t table = sizeof(float2) * (size_t)d.max_ctx * (d.head_dim / 2);
+  if (cudaMalloc(&c->region, 256 + table) != cudaSuccess) {
+    cudaGetLastError();
+    delete c;
+    return MK_ERR_CUDA;
+  }
+  mk::CacheView& w = c->view;
+  w.B = d.batch;
+  w.nq = d.n_q_heads;
+  w.nkv = d.n_kv_heads;
+  w.hd = d.head_dim;
+  w.T = d.max_ctx;
+  w.L = d.n_layers;
+  w.bt = kv->block_table;
+  if (w.bt) {
+    w.page = kv->page_size;
+    w.n_pages = kv->n_pages;
+    w.bt_stride = (int)(((int64_t)d.max_ctx + kv->page_size - 1) / kv->page_size);
+  }
+  w.status = (int*)c->region;
+  c->rope = (float2*)((uint8_t*)c->region + 256);
+  mk::rope_table<<<n_sm * 4, 256>>>(c->rope, d.max_ctx, d.head_dim / 2, (double)d.rope_theta);
+  // the table is ready when this returns: calls may come on any stream
+  if (cudaGetLastError() != cudaSuccess || cudaMemset(c->region, 0, 256) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(c->region);
+    delete c;
+    return MK_ERR_CUDA;
+  }
+  *out = c;
+  return MK_OK;
+}
+
+extern "C" int mk_cache_destroy(mk_cache* c) {
+  if (!c) return MK_OK;
+  int dev = c->device, now = dev;
+  cudaGetDevice(&now);
+  if (now != dev) cudaSetDevice(dev);
+  const cudaError_t e = cudaFree(c->region);
+  if (now != dev) cudaSetDevice(now);
+  delete c;
+  return mk::launched(e);
+}
+
+extern "C" int mk_cache_get_status(mk_cache* c, void* stream) {
+  if (!c) return MK_ERR_INVALID_ARG;
+  if (int rc = mk::on_device(c)) return rc;
+  int st[2] = {0, 0};
+  cudaStream_t s = (cudaStream_t)stream;
+  if (cudaMemcpyAsync(st, c->view.status, sizeof(st), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess ||
+      (st[0] && (cudaMemsetAsync(c->view.status, 0, sizeof(st), s) != cudaSuccess ||
+                 cudaStreamSynchronize(s) != cudaSuccess))) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return st[0];
+}
+
+extern "C" int mk_cache_append(mk_cache* c, int layer, const mk_append_args* a, void* stream) {
+  if (!c || !a || layer < 0 || layer >= c->d.n_layers || a->n_tokens < 0 ||
+      (!a->starts && a->n_tokens != c->d.batch) || (a->dtype != MK_DTYPE_BF16 && a->dtype != MK_DTYPE_FP32))
+    return MK_ERR_INVALID_ARG;
+  if (a->n_tokens == 0) return MK_OK;
+  if (!a->k || !a->v || !a->seq_lens || !a->q != !a->q_out) return MK_ERR_INVALID_ARG;
+  const int64_t es = a->dtype == MK_DTYPE_BF16 ? 2 : 4;
+  if ((a->q && (!mk::aligned(a->q, 16) || !mk::aligned(a->q_out, 16) || (a->q_stride * es) % 16)) ||
+      !mk::aligned(a->k, 16) || !mk::aligned(a->v, 16) || (a->k_stride * es) % 16 || (a->v_stride * es) % 16 ||
+      !mk::aligned(a->q_norm, 16) || !mk::aligned(a->k_norm, 16) || !mk::aligned(a->starts, 4) ||
+      !mk::aligned(a->seq_lens, 4) || !mk::aligned(a->positions, 4))
+    return MK_ERR_UNSUPPORTED;
+  if (int rc = mk::on_device(c)) return rc;
+  return mk::launched(mk::append(*c, layer, *a, (cudaStream_t)stream));
+}
+
+extern "C" size_t mk_cache_attend_bytes(const mk_cache* c) { return c ? mk::attend_workspace(c->d, c->n_sm) : 0; }
+
+extern "C" int mk_cache_attend(mk_cache* c, int layer, const void* q, const int32_t* seq_lens, int prefix_len,
+                               float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!c || !q || !seq_lens || !out || !workspace) return MK_ERR_INVALID_ARG;
+  if (layer < 0 || layer >= c->d.n_layers || prefix_len < 0 || prefix_len > c->d.max_ctx || !isfinite(scale) ||
+      workspace_bytes < mk::attend_workspace(c->d, c->n_sm))
+    return MK_ERR_INVALID_ARG;
+  if (!mk::aligned(q, 16) || !mk::aligned(out, 16) || !mk::aligned(seq_lens, 4) || !mk::aligned(lse, 4) ||
+      !mk::aligned(workspace, 256))
+    return MK_ERR_UNSUPPORTED;
+  if (int rc = mk::on_device(c)) return rc;
+  return mk::launched(mk::attend(*c, layer, q, seq_lens, prefix_len, scale, out, lse, workspace, (cudaStream_t)stream));
+}

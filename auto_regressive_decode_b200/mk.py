@@ -27,6 +27,9 @@ MK_STATE_EXPERT_COUNT = 4
 MK_STATE_TRACE = 5
 MK_STATE_COUNTERS = 6
 
+MK_DTYPE_BF16 = 0
+MK_DTYPE_FP32 = 1
+
 OP_NAMES = {0: "nop", 1: "embed", 2: "qkv", 3: "attn", 4: "oproj", 5: "gateup", 6: "down", 7: "lmhead",
             8: "router", 9: "exp_gateup", 10: "exp_down"}
 
@@ -53,6 +56,17 @@ class mk_kv(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("block_table", _P), ("page_size", _i32), ("n_pages", _i32)]
 
 
+class mk_cache_desc(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("n_layers", "batch", "n_q_heads", "n_kv_heads", "head_dim", "max_ctx")] + \
+               [("rms_eps", _f32), ("rope_theta", _f32)]
+
+
+class mk_append_args(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("q", "k", "v")] + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [(n, _P) for n in ("starts", "seq_lens", "positions", "q_norm", "k_norm", "q_out")] + \
+               [("n_tokens", _i32), ("dtype", _i32)]
+
+
 class mk_instr(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("op_layer", "wait_idx", "wait_count", "sig_idx", "a", "b", "c", "d")]
 
@@ -74,6 +88,15 @@ def _load():
         "mk_state_bytes": (ctypes.c_size_t, [H, _i32]),
         "mk_decode_step_noalloc": (_i32, [ctypes.POINTER(mk_model_desc), ctypes.POINTER(mk_weights),
                                           ctypes.POINTER(mk_kv), _P, _P, _P, _P, _P]),
+        "mk_cache_create": (_i32, [ctypes.POINTER(mk_cache_desc), ctypes.POINTER(mk_kv), ctypes.POINTER(H)]),
+        "mk_cache_destroy": (_i32, [H]),
+        "mk_cache_get_status": (_i32, [H, _P]),
+        "mk_cache_append": (_i32, [H, _i32, ctypes.POINTER(mk_append_args), _P]),
+        "mk_cache_attend": (_i32, [H, _i32, _P, _P, _i32, _f32, _P, _P, _P, ctypes.c_size_t, _P]),
+        "mk_cache_attend_bytes": (ctypes.c_size_t, [H]),
+        "mk_token_logprobs": (_i32, [_P, _i32, ctypes.c_int64, _i32, _i32, _P, _P, _P, _i32, _P, _P, _P]),
+        "mk_decode_greedy_scored": (_i32, [H, ctypes.POINTER(mk_model_desc), _i32, _P, _P, _P, _P, _P, _P, _P, _P, _i32,
+                                           _P, _P]),
         "mk_plan_create": (_i32, [ctypes.POINTER(mk_model_desc), _i32, ctypes.POINTER(H)]),
         "mk_plan_n_sm": (_i32, [H]),
         "mk_plan_n_counters": (_i32, [H]),
@@ -102,6 +125,14 @@ mk_destroy = lib.mk_destroy
 mk_read_state = lib.mk_read_state
 mk_state_bytes = lib.mk_state_bytes
 mk_decode_step_noalloc = lib.mk_decode_step_noalloc
+mk_cache_create = lib.mk_cache_create
+mk_cache_destroy = lib.mk_cache_destroy
+mk_cache_get_status = lib.mk_cache_get_status
+mk_cache_append = lib.mk_cache_append
+mk_cache_attend = lib.mk_cache_attend
+mk_cache_attend_bytes = lib.mk_cache_attend_bytes
+mk_token_logprobs = lib.mk_token_logprobs
+mk_decode_greedy_scored = lib.mk_decode_greedy_scored
 mk_plan_create = lib.mk_plan_create
 mk_plan_n_sm = lib.mk_plan_n_sm
 mk_plan_n_counters = lib.mk_plan_n_counters
@@ -238,6 +269,31 @@ class Decoder:
         check(mk_decode_greedy(self.h, n_steps, tokens.data_ptr(), seq_lens.data_ptr(), s, out_tokens.data_ptr(),
                                None if logits is None else logits.data_ptr()), "mk_decode_greedy")
 
+    def greedy_scored(self, n_steps, tokens, seq_lens, out_tokens, top_k=0, logits=None, stream=None):
+        """greedy() with the scores of every picked token (asynchronous): (logprob [n][B], entropy [n][B], top ids
+        int32 [n][B][top_k], their log probabilities, lengths after the loop int32 [B]); see token_logprobs.  logits:
+        float32 [B][vocab] working buffer, the last step's logits afterwards."""
+        torch = self.torch
+        st = stream or torch.cuda.current_stream()
+        B, V = self.cfg.batch, self.cfg.vocab
+        with torch.cuda.stream(st):
+            lg = torch.empty((B, V), dtype=torch.float32, device="cuda") if logits is None else logits
+            lens = torch.empty((B,), dtype=torch.int32, device="cuda")
+            logprob, entropy = torch.empty((2, n_steps, B), dtype=torch.float32, device="cuda")
+            ids = torch.empty((n_steps, B, top_k), dtype=torch.int32, device="cuda")
+            tops = torch.empty((n_steps, B, top_k), dtype=torch.float32, device="cuda")
+        check(mk_decode_greedy_scored(self.h, ctypes.byref(self.desc), n_steps, tokens.data_ptr(), seq_lens.data_ptr(),
+                                      st.cuda_stream, out_tokens.data_ptr(), lens.data_ptr(), lg.data_ptr(),
+                                      logprob.data_ptr(), entropy.data_ptr(), top_k, ids.data_ptr(), tops.data_ptr()),
+              "mk_decode_greedy_scored")
+        return logprob, entropy, ids, tops, lens
+
+    def cache(self):
+        """A Cache of this decoder's KV cache: rows appended through it are the ones its steps attend over."""
+        c, (_, k, v, table) = self.cfg, self._keep
+        return Cache(k, v, n_q_heads=c.n_q_heads, batch=c.batch, max_ctx=c.max_ctx, block_table=table,
+                     page_size=0 if table is None else k.shape[3], rope_theta=c.rope_theta, rms_eps=c.rms_eps)
+
     def status(self, stream=None):
         s = (stream or self.torch.cuda.current_stream()).cuda_stream
         return mk_get_status(self.h, s)
@@ -283,6 +339,175 @@ class Decoder:
             self.close()
         except Exception:
             pass
+
+
+# ---- operators on the KV cache, and scores of tokens ----------------------------------------------
+
+def _require(ok, what):
+    if not ok:
+        raise MkError(MK_ERR_INVALID_ARG, what)
+
+
+def _dtype(t, what):
+    name = str(t.dtype)
+    _require(name in ("torch.bfloat16", "torch.float32"), f"{what}: bf16 or fp32 is wanted, got {name}")
+    return MK_DTYPE_BF16 if name == "torch.bfloat16" else MK_DTYPE_FP32
+
+
+def _int32(t, shape, device, what):
+    import torch
+    _require(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == device and t.is_contiguous(),
+             f"{what}: a contiguous int32 tensor of shape {shape} on {device} is wanted")
+    return t.data_ptr()
+
+
+class Cache:
+    """Owns one mk_cache: the append and attend operators on a KV cache.
+
+    k, v: device bf16 [L][B][n_kv][max_ctx][hd], or with block_table (device int32
+    [B][ceil(max_ctx/page_size)]) page pools [L][n_pages][n_kv][page_size][hd]; page_size a multiple of 16.
+    Calls are asynchronous; tensors must stay alive until the stream has used them, and they and the stream
+    belong to the cache's device."""
+
+    def __init__(self, k, v, n_q_heads, batch, max_ctx, block_table=None, page_size=0, rope_theta=1e4, rms_eps=1e-6):
+        import torch
+        self.torch = torch
+        _require(k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.dim() == 5 and k.is_cuda and
+                 v.device == k.device and k.is_contiguous() and v.is_contiguous(),
+                 "Cache: k and v are contiguous bf16 device tensors of one shape [.][.][.][.][.]")
+        L, n, nkv, rows, hd = k.shape
+        self.device = k.device
+        table = None
+        if block_table is None:
+            _require(n == batch and rows == max_ctx, f"Cache: k of shape [L][{batch}][n_kv][{max_ctx}][hd] is wanted")
+            kv = mk_kv(k.data_ptr(), v.data_ptr(), None, 0, 0)
+        else:
+            _require(rows == page_size > 0, f"Cache: k of shape [L][n_pages][n_kv][{page_size}][hd] is wanted")
+            table = _int32(block_table, (batch, -(-max_ctx // page_size)), k.device, "Cache: block_table")
+            kv = mk_kv(k.data_ptr(), v.data_ptr(), table, page_size, n)
+        self._keep = (k, v, block_table)
+        self.n_layers, self.batch, self.max_ctx = L, batch, max_ctx
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, nkv, hd
+        self._q_shape = (batch, n_q_heads, hd)
+        desc = mk_cache_desc(L, batch, n_q_heads, nkv, hd, max_ctx, rms_eps, rope_theta)
+        h = _P()
+        with torch.cuda.device(self.device):
+            check(mk_cache_create(ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(h)), "mk_cache_create")
+        self.h = h
+        self._ws_bytes = mk_cache_attend_bytes(h)
+
+    def _rows(self, t, n, heads, dtype, what):
+        """Pointer and token stride of [n][heads][hd] whose heads are contiguous within a token."""
+        hd = self.head_dim
+        _require(t.shape == (n, heads, hd) and t.dtype == dtype and t.device == self.device and
+                 (t.stride(2) == 1 and (t.stride(1) == hd or heads == 1) or n == 0),
+                 f"append: {what} of shape ({n}, {heads}, {hd}), {dtype}, heads contiguous, on {self.device} is wanted")
+        return t.data_ptr(), t.stride(0)
+
+    def append(self, layer, k, v, seq_lens, q=None, starts=None, positions=None, q_norm=None, k_norm=None, q_out=None,
+               stream=None):
+        """Append keys and values (bf16 or fp32 [n][n_kv][hd]) to the cache, the keys rotated; returns the rotated
+        q (bf16 [n][n_q][hd]) where q is given.  seq_lens int32 [B]: rows held before; starts int32 [B + 1]: the
+        tokens of each sequence (None: one each); see mk_cache_append."""
+        torch, dev = self.torch, self.device
+        st = stream or torch.cuda.current_stream(dev)
+        n = k.shape[0]
+        dt = _dtype(k, "append")
+        a = mk_append_args()
+        a.k, a.k_stride = self._rows(k, n, self.n_kv_heads, k.dtype, "k")
+        a.v, a.v_stride = self._rows(v, n, self.n_kv_heads, k.dtype, "v")
+        if q is not None:
+            a.q, a.q_stride = self._rows(q, n, self.n_q_heads, k.dtype, "q")
+            if q_out is None:
+                with torch.cuda.stream(st):
+                    q_out = torch.empty((n, self.n_q_heads, self.head_dim), dtype=torch.bfloat16, device=dev)
+            _require(q_out.shape == q.shape and q_out.dtype == torch.bfloat16 and q_out.device == dev and
+                     q_out.is_contiguous(), "append: q_out")
+            a.q_out = q_out.data_ptr()
+        else:
+            _require(q_out is None, "append: q_out without q")
+        if starts is not None:
+            a.starts = _int32(starts, (self.batch + 1,), dev, "append: starts")
+        else:
+            _require(n == self.batch, f"append: {self.batch} tokens are wanted without starts")
+        a.seq_lens = _int32(seq_lens, (self.batch,), dev, "append: seq_lens")
+        if positions is not None:
+            a.positions = _int32(positions, (n,), dev, "append: positions")
+        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if g is not None:
+                _require(g.shape == (self.head_dim,) and g.dtype == torch.bfloat16 and g.device == dev and
+                         g.is_contiguous(), f"append: {name}")
+                setattr(a, name, g.data_ptr())
+        a.n_tokens, a.dtype = n, dt
+        self._call(mk_cache_append, "mk_cache_append", layer, ctypes.byref(a), st.cuda_stream)
+        return q_out
+
+    def attend(self, layer, q, seq_lens, prefix_len=0, scale=0.0, out=None, lse=None, workspace=None, stream=None):
+        """Attention of one query token a sequence, q bf16 [B][n_q][hd], over the first seq_lens[b] rows; the rows
+        below prefix_len are sequence 0's for all.  Returns (out bf16 [B][n_q][hd], lse fp32 [B][n_q]); see
+        mk_cache_attend."""
+        torch, dev, shape = self.torch, self.device, self._q_shape
+        st = stream or torch.cuda.current_stream(dev)
+        _require(q.shape == shape and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous(),
+                 f"attend: a contiguous bf16 q of shape {shape} on {dev} is wanted")
+        lens = _int32(seq_lens, (self.batch,), dev, "attend: seq_lens")
+        if out is None or lse is None or workspace is None:
+            with torch.cuda.stream(st):
+                out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
+                lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
+                if workspace is None:
+                    workspace = torch.empty((self._ws_bytes,), dtype=torch.uint8, device=dev)
+        _require(out.shape == shape and out.dtype == torch.bfloat16 and out.device == dev and out.is_contiguous() and
+                 lse.shape == shape[:2] and lse.dtype == torch.float32 and lse.device == dev and lse.is_contiguous() and
+                 workspace.device == dev and workspace.is_contiguous(), "attend: out, lse, workspace")
+        self._call(mk_cache_attend, "mk_cache_attend", layer, q.data_ptr(), lens, prefix_len, scale, out.data_ptr(),
+                   lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
+        return out, lse
+
+    def _call(self, fn, name, *args):
+        torch = self.torch
+        if torch.cuda.current_device() == self.device.index:
+            return check(fn(self.h, *args), name)
+        with torch.cuda.device(self.device):
+            return check(fn(self.h, *args), name)
+
+    def status(self, stream=None):
+        """First error recorded on the device since the last call (synchronises the stream)."""
+        with self.torch.cuda.device(self.device):
+            return mk_cache_get_status(self.h, (stream or self.torch.cuda.current_stream()).cuda_stream)
+
+    def close(self):
+        if getattr(self, "h", None):
+            mk_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def token_logprobs(logits, tokens, top_k=0, stream=None):
+    """Scores of tokens (int32 [n]) under logits (bf16 or fp32 [n][vocab], rows any stride apart): (logprob fp32
+    [n], entropy fp32 [n], ids int32 [n][top_k], their log probabilities fp32 [n][top_k]); see mk_token_logprobs."""
+    import torch
+    _require(logits.dim() == 2 and logits.is_cuda and (logits.stride(1) == 1 or logits.shape[1] == 1),
+             "token_logprobs: device logits [n][vocab] with contiguous rows are wanted")
+    dt, dev, (n, V) = _dtype(logits, "token_logprobs"), logits.device, logits.shape
+    st = stream or torch.cuda.current_stream(dev)
+    tok = _int32(tokens, (n,), dev, "token_logprobs: tokens")
+    _require(0 <= top_k <= 32, "token_logprobs: top_k 0..32 is wanted")
+    with torch.cuda.stream(st):
+        scores = torch.empty((2, n), dtype=torch.float32, device=dev)
+        ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        tops = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+    logprob, entropy = scores[0], scores[1]
+    args = (logits.data_ptr(), dt, logits.stride(0), n, V, tok, logprob.data_ptr(), entropy.data_ptr(), top_k,
+            ids.data_ptr(), tops.data_ptr(), st.cuda_stream)
+    with torch.cuda.device(dev):
+        check(mk_token_logprobs(*args), "mk_token_logprobs")
+    return logprob, entropy, ids, tops
 
 
 def weight_structs(cfg, weights, k_cache, v_cache):

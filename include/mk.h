@@ -220,6 +220,139 @@ int mk_decode_step_noalloc(const mk_model_desc* desc, const mk_weights* weights,
                            const int32_t* tokens, const int32_t* positions, const int32_t* seq_lens, void* stream,
                            float* out_logits);
 
+/* ---- operators on the KV cache, and scores of tokens ------------------------
+ *
+ * The decode step appends one row a sequence and attends inside its kernel.
+ * These entry points do the work around it: filling a cache with many rows,
+ * attending for batches that share a long prefix, and scoring tokens.  They
+ * follow the conventions above: asynchronous on `stream`, no allocation and no
+ * host synchronisation after mk_cache_create, safe in stream capture.
+ *
+ * A cache handle describes a cache (the same layouts as mk_kv; page_size is a
+ * multiple of 16 here) and holds its rotation table and tensor maps.  It may
+ * describe the cache of an mk_handle.  The calls only read it, so calls on
+ * several streams may overlap as far as their buffers allow: an attend reads
+ * what an earlier append of the same stream wrote, and overlapping attends
+ * need a workspace each.
+ */
+typedef struct mk_cache_desc {
+  int32_t n_layers, batch, n_q_heads, n_kv_heads, head_dim, max_ctx;
+  float rms_eps, rope_theta;
+} mk_cache_desc;
+typedef struct mk_cache mk_cache;
+
+/*
+ * Returns MK_ERR_UNSUPPORTED for head_dim not 64 or 128, more than 64 query
+ * heads per KV head or a number that n_kv_heads does not divide, batch above
+ * 1024, a page_size that is not a multiple of 16, caches of 2^31 rows
+ * (head_dim elements each) or more, misaligned pointers (16 bytes), and
+ * MK_ERR_INVALID_ARG for malformed sizes.  The caches and the block table are
+ * borrowed.
+ */
+int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_cache** out);
+/* Waits for the device's work on the handle.  NULL is accepted. */
+int mk_cache_destroy(mk_cache* c);
+/* Synchronise `stream` and return the first error that calls recorded on the
+ * device (MK_OK, MK_ERR_RANGE, MK_ERR_DEVICE_TIMEOUT); the error is cleared.
+ * Later calls work as before: a range error concerns the sequences or tokens
+ * with the value out of range, and no memory outside the caller's buffers is
+ * read or written because of it. */
+int mk_cache_get_status(mk_cache* c, void* stream);
+
+enum { MK_DTYPE_BF16 = 0, MK_DTYPE_FP32 = 1 };
+
+/*
+ * Append the keys and values of n_tokens tokens to `layer` of the cache,
+ * rotating the keys (rotate-half pairs, angle pos * rope_theta^(-2i/head_dim))
+ * and, if given, the queries.
+ *   q, k, v   device [n_tokens][heads][head_dim] of `dtype` (bf16 or fp32),
+ *             the heads of a token contiguous, `*_stride` elements from a
+ *             token to the next (a fused projection's buffer works); q may be
+ *             NULL.  Pointers and strides in bytes are multiples of 16.
+ *   starts    device int32[batch+1], ascending: tokens [starts[b], starts[b+1])
+ *             belong to sequence b (none or many); tokens outside
+ *             [starts[0], starts[batch]) are left out.  NULL: n_tokens ==
+ *             batch, one token a sequence.
+ *   seq_lens  device int32[batch]: rows sequence b holds before the call; its
+ *             tokens go to rows seq_lens[b], seq_lens[b]+1, ...
+ *   positions device int32[n_tokens]: rotation positions, each in
+ *             [0, max_ctx); NULL: the row's index
+ *   q_norm, k_norm device bf16[head_dim] or NULL: RMSNorm (rms_eps) of each
+ *             query / key head with this gain before the rotation
+ *   q_out     device bf16 [n_tokens][n_q_heads][head_dim], with q
+ * Arithmetic is fp32; each result is rounded once, to bf16.  A token whose row
+ * is outside [0, max_ctx), whose page is outside the pool or whose position is
+ * out of range is not written (MK_ERR_RANGE).  No two tokens of a call share a
+ * row unless the block table maps two sequences' new rows to one page.
+ */
+typedef struct mk_append_args {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *starts, *seq_lens, *positions;
+  const void *q_norm, *k_norm;
+  void* q_out;
+  int32_t n_tokens, dtype;
+} mk_append_args;
+int mk_cache_append(mk_cache* c, int layer, const mk_append_args* args, void* stream);
+
+/*
+ * Attention of one query token a sequence over `layer` of the cache.
+ * Sequence b attends positions [0, seq_lens[b]) (its new row included when it
+ * is appended).  Positions below prefix_len are read from sequence 0's rows
+ * (its pages) for every sequence, once for all of them; sequence b's own rows
+ * there are not read.  prefix_len 0: nothing is shared.
+ *   q         device bf16 [batch][n_q_heads][head_dim] (rotated), head j reads
+ *             KV head j / (n_q_heads / n_kv_heads)
+ *   seq_lens  device int32[batch], each in [0, max_ctx]; a sequence of length 0
+ *             gets zeros and lse -infinity, one shorter than the prefix attends
+ *             its part of it
+ *   scale     of the scores; 0: 1/sqrt(head_dim)
+ *   out       device bf16 [batch][n_q_heads][head_dim]
+ *   lse       device fp32 [batch][n_q_heads]: natural logarithm of the softmax
+ *             sums, or NULL
+ *   workspace device, 256-byte aligned, mk_cache_attend_bytes(c) bytes; its
+ *             contents before and after the call do not matter
+ * Scores, softmax sums and output sums are fp32; the probabilities are rounded
+ * to bf16 as operands of the second product.
+ */
+int mk_cache_attend(mk_cache* c, int layer, const void* q, const int32_t* seq_lens, int prefix_len, float scale,
+                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+size_t mk_cache_attend_bytes(const mk_cache* c);
+
+/*
+ * Scores of given tokens and the most likely alternatives, from logits.
+ *   logits    device [n_rows][vocab] of `dtype`, `row_stride` elements from a row to the next
+ *   tokens    device int32[n_rows]
+ *   out_logprob  device fp32[n_rows]: logits[token] - logsumexp(row); NaN for a
+ *             token outside [0, vocab)
+ *   out_entropy  device fp32[n_rows] or NULL: of the row's distribution, in nats
+ *   out_top_ids, out_top_logprobs  device int32 / fp32 [n_rows][top_k], best
+ *             first, the lower id first among equal logits; top_k 0..32
+ *             (NULL when 0)
+ * Logits of -infinity have probability 0 and are no alternatives: missing
+ * alternatives are id -1, log probability -infinity.  A row that holds a NaN
+ * or +infinity, or nothing but -infinity, has no distribution: its scores are
+ * NaN and its ids -1.  Any alignment of rows.
+ */
+int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_rows, int vocab, const int32_t* tokens,
+                      float* out_logprob, float* out_entropy, int top_k, int32_t* out_top_ids,
+                      float* out_top_logprobs, void* stream);
+
+/*
+ * mk_decode_greedy with the scores of every picked token, mk_token_logprobs of
+ * each step's logits.  `desc` is the one the handle was created with.
+ *   out_lens   device int32[batch]: the lengths after the loop (also its
+ *              working state; not the array seq_lens)
+ *   logits     device fp32[batch][vocab]: the last step's logits afterwards
+ *   out_logprob, out_entropy  device fp32 [n_steps][batch]; out_top_*  device
+ *              [n_steps][batch][top_k], as above.  A step that failed has
+ *              token -1 and logprob NaN.
+ */
+int mk_decode_greedy_scored(mk_handle* h, const mk_model_desc* desc, int n_steps, const int32_t* tokens,
+                            const int32_t* seq_lens, void* stream, int32_t* out_tokens, int32_t* out_lens,
+                            float* logits, float* out_logprob, float* out_entropy, int top_k, int32_t* out_top_ids,
+                            float* out_top_logprobs);
+
 /* ---- host-only lowering (no GPU needed) ---------------------------------- */
 
 /* One instruction of a per-SM list (8 x int32); see mk_plan_* below. */

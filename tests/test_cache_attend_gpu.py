@@ -1,0 +1,231 @@
+"""mk_cache_attend against attention in 64 bits.
+
+Tolerance of an output o = sum p v / l with A = sum p |v| / l: the result is
+rounded to bf16 (2^-8 |o|) and so is every probability (2^-8 A).  In fp32, a
+score sums head_dim exact products: it is off by at most (head_dim + 2) 2^-24
+of scale sum |q k| = S, which moves every p by that much of itself, p and l by
+2^-21 of the exponential, and the output's sum by 2^-24 per term of a run of
+tiles: 2^-12 A + 2 (head_dim + 2) 2^-24 S A covers them.  lse moves by (head_dim + 2) 2^-24 S + 2^-18.
+
+Every cache row that the operator has no business reading holds NaN.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def make(batch, nq, nkv, hd, page, prefix, lens, seed=0, n_layers=2, layer=1, max_ctx=None, q_scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    max_ctx = max_ctx or max(max(lens), prefix, 1) + 5
+    nan = float("nan")
+
+    def rows():  # each sequence's own rows; NaN behind its length, and below the prefix (sequence 0 apart)
+        r = torch.randn((batch, nkv, max_ctx, hd), generator=g, device="cuda").bfloat16()
+        for b, n in enumerate(lens):
+            r[b, :, n if b else max(n, min(prefix, max(lens))):] = nan
+            if b:
+                r[b, :, :prefix] = nan
+        if lens[0] <= prefix:
+            r[0, :, min(prefix, max(lens)):] = nan
+        return r
+    s = dict(batch=batch, nq=nq, nkv=nkv, hd=hd, page=page, prefix=prefix, lens=lens, max_ctx=max_ctx, layer=layer, kr=rows(), vr=rows())
+    s["q"] = (torch.randn((batch, nq, hd), generator=g, device="cuda") * q_scale).bfloat16()
+    s["seq_lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    s["table"] = None
+    for w in ("k", "v"):
+        src = s[w + "r"]
+        if page:
+            stride = -(-max_ctx // page)
+            pool = batch * stride + 3
+            if s["table"] is None:
+                table = torch.randperm(pool, generator=g, device="cuda").int()[:batch * stride].view(batch, stride).contiguous()
+                s["table"] = table
+            t = torch.full((n_layers, pool, nkv, page, hd), nan, dtype=torch.bfloat16, device="cuda")
+            for b in range(batch):
+                for j in range(stride):
+                    part = src[b, :, j * page:(j + 1) * page]
+                    t[layer, int(s["table"][b, j]), :, :part.shape[1]] = part
+        else:
+            t = torch.full((n_layers, batch, nkv, max_ctx, hd), nan, dtype=torch.bfloat16, device="cuda")
+            t[layer] = src
+        s[w] = t
+    if page:  # pages a sequence has no business with are outside the pool
+        for b, n in enumerate(lens):
+            for j in range(s["table"].shape[1]):
+                lo, hi = j * page, (j + 1) * page
+                if not (b == 0 and lo < min(prefix, max(lens)) or n > prefix and lo < n and hi > prefix):
+                    s["table"][b, j] = -1
+    return s
+
+
+def handle(s):
+    import auto_regressive_decode_b200.mk as mk
+    return mk.Cache(s["k"], s["v"], n_q_heads=s["nq"], batch=s["batch"], max_ctx=s["max_ctx"], block_table=s["table"], page_size=s["page"])
+
+
+def check(s, out, lse, scale=None):
+    hd, g, p = s["hd"], s["nq"] // s["nkv"], s["prefix"]
+    scale = scale or hd ** -0.5
+    assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+    for b, n in enumerate(s["lens"]):
+        if n == 0:
+            assert (out[b] == 0).all() and (lse[b] == -math.inf).all()
+            continue
+        q = s["q"][b].double().view(s["nkv"], g, hd)
+        k, v = (torch.cat([s[w][0, :, :min(n, p)], s[w][b, :, p:max(n, p)]], 1).double() for w in ("kr", "vr"))
+        sc = q @ k.transpose(1, 2) * scale
+        size = ((q.abs() @ k.abs().transpose(1, 2)) * abs(scale)).amax(-1, keepdim=True)
+        w = torch.softmax(sc, -1)
+        o, a = w @ v, w @ v.abs()
+        tol = 2 ** -8 * (o.abs() + a) + 2 ** -12 * a + 2 * (hd + 2) * 2 ** -24 * size * a
+        err = (out[b].double().view(o.shape) - o).abs()
+        assert (err <= tol).all(), (b, float((err / tol).max()))
+        le = (lse[b].double().view(o.shape[:2]) - torch.logsumexp(sc, -1)).abs()
+        assert (le <= (hd + 2) * 2 ** -24 * size[..., 0] + 2 ** -18).all(), (b, float(le.max()))
+
+
+CASES = [
+    # batch, nq, nkv, hd, page, prefix, lens
+    (1, 1, 1, 64, 0, 0, [1]),
+    (1, 4, 2, 128, 0, 0, [129]),
+    (1, 16, 8, 128, 16, 100, [101]),
+    (1, 8, 1, 128, 128, 128, [128]),                                   # the prefix is all
+    (2, 4, 2, 64, 0, 5, [6, 5]),                                       # one has nothing of its own
+    (3, 6, 2, 64, 48, 50, [0, 51, 200]),                               # an idle slot 0: the prefix is still its rows
+    (3, 8, 8, 128, 16, 130, [130, 7, 300]),                            # shorter than the prefix
+    (4, 32, 4, 128, 32, 17, [18, 400, 17, 145]),
+    (5, 10, 2, 128, 128, 640, [641, 700, 0, 1000, 640]),
+    (2, 64, 1, 128, 16, 33, [40, 1000]),                               # 64 heads on one KV head
+    (2, 17, 1, 64, 0, 200, [201, 333]),
+    (8, 40, 40, 128, 128, 300, [301, 1024, 555, 310, 900, 301, 777, 428]),
+    (33, 16, 4, 64, 16, 1000, [1000 + i for i in range(33)]),          # 132 rows of a KV head share the prefix
+    (40, 8, 1, 128, 0, 500, [500 + 13 * i for i in range(40)]),
+    (130, 4, 2, 128, 64, 257, [i * 3 for i in range(130)]),            # many shorter than the prefix
+    (300, 2, 2, 64, 16, 31, [i % 47 for i in range(300)]),
+    (4, 8, 2, 128, 64, 1000, [0, 300, 299, 10]),                       # the prefix is longer than every sequence
+    (3, 4, 4, 64, 16, 64, [0, 0, 0]),
+    (2, 8, 2, 64, 384, 5000, [5001, 9000]),
+]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_attend_matches_the_definition(case):
+    s = make(*case, seed=1)
+    c = handle(s)
+    out, lse = c.attend(s["layer"], s["q"], s["seq_lens"], prefix_len=s["prefix"])
+    assert c.status() == 0
+    check(s, out, lse)
+
+
+def test_sharing_changes_nothing_but_roundings():
+    """The same sequences with the prefix read from sequence 0, and each with its own copy of it."""
+    s = make(6, 16, 4, 128, 16, 600, [600 + 50 * i + 1 for i in range(6)], seed=2)
+    c = handle(s)
+    out, lse = c.attend(1, s["q"], s["seq_lens"], prefix_len=600)
+    check(s, out, lse)
+    full = torch.cat([s["kr"][:1, :, :600].expand(6, -1, -1, -1), s["kr"][:, :, 600:]], 2), \
+        torch.cat([s["vr"][:1, :, :600].expand(6, -1, -1, -1), s["vr"][:, :, 600:]], 2)
+    t = dict(s, page=0, table=None, prefix=0, kr=full[0], vr=full[1],
+             k=torch.stack([full[0]] * 2).contiguous(), v=torch.stack([full[1]] * 2).contiguous())
+    out2, lse2 = handle(t).attend(1, s["q"], s["seq_lens"])
+    check(t, out2, lse2)
+
+
+@pytest.mark.parametrize("scale", [0.5, 3.0, -0.1])
+def test_scale_and_large_scores(scale):
+    s = make(3, 8, 2, 64, 16, 100, [101, 180, 340], seed=3, q_scale=4.0)
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=100, scale=scale)
+    check(s, out, lse, scale)
+
+
+def test_equal_keys_give_the_mean_value():
+    s = make(2, 4, 2, 64, 0, 128, [129, 400], seed=4)
+    for w in ("k", "kr"):
+        s[w].copy_(torch.where(torch.isnan(s[w]), s[w], torch.ones_like(s[w])))
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=128)
+    check(s, out, lse)
+
+
+def test_infinite_and_nan_rows_that_are_attended_spread():
+    s = make(2, 4, 2, 64, 0, 10, [11, 40], seed=5)
+    s["v"][1, 1, 0, 20, 3] = float("inf")
+    s["v"][1, 0, 1, 4, 5] = float("nan")          # in the prefix: both sequences attend it
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=10)
+    o = out.view(2, 2, 2, 64)
+    assert torch.isinf(o[1, 0, :, 3]).all() and torch.isnan(o[:, 1, :, 5]).all()
+    o = o.clone()
+    o[1, 0, :, 3] = 0
+    o[:, 1, :, 5] = 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+def test_bad_lengths_and_pages_are_reported():
+    import auto_regressive_decode_b200.mk as mk
+    s = make(3, 4, 2, 64, 16, 20, [30, 41, 25], seed=6)
+    c = handle(s)
+    for bad in (-1, s["max_ctx"] + 1):
+        lens = s["seq_lens"].clone()
+        lens[1] = bad
+        full = s["table"].clone()
+        s["table"].clamp_(min=0)                   # every page readable: only the length is wrong
+        out, lse = c.attend(1, s["q"], lens, prefix_len=20)
+        assert c.status() == mk.MK_ERR_RANGE and c.status() == mk.MK_OK
+        s["table"].copy_(full)
+        ok = {w: s[w] for w in s}
+        for b in (0, 2):                           # the others are as ever
+            check(dict(ok, lens=[s["lens"][x] if x == b else 0 for x in range(3)]),
+                  torch.where(torch.arange(3, device="cuda")[:, None, None] == b, out, 0),
+                  torch.where(torch.arange(3, device="cuda")[:, None] == b, lse, -math.inf))
+    s["table"][1, 2] = s["k"].shape[1]             # rows 32..47 of sequence 1
+    c.attend(1, s["q"], s["seq_lens"], prefix_len=20)
+    assert c.status() == mk.MK_ERR_RANGE
+
+
+def test_overlapping_calls_and_captured_graphs():
+    s = make(4, 8, 2, 128, 16, 200, [201, 300, 0, 250], seed=7)
+    c = handle(s)
+    q2 = (s["q"].float() * 0.5).bfloat16()
+    want = [c.attend(1, q, s["seq_lens"], prefix_len=200) for q in (s["q"], q2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got += [c.attend(1, q, s["seq_lens"], prefix_len=200, stream=st) for q, st in zip((s["q"], q2), streams)]
+    graphs = []
+    for q in (s["q"], q2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, c.attend(1, q, s["seq_lens"], prefix_len=200)))
+    for _ in range(5):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    got += [graphs[0][1], graphs[1][1]]
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
+    # a captured call follows lengths rewritten between replays
+    s["lens"] = [201, 240, 0, 215]
+    s["seq_lens"].copy_(torch.tensor(s["lens"], dtype=torch.int32))
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    check(s, *graphs[0][1])
+    assert c.status() == 0
+
+
+def test_caller_buffers_and_same_bits_every_time():
+    s = make(9, 16, 2, 64, 32, 400, [401 + 37 * i for i in range(9)], seed=9)
+    c = handle(s)
+    out = torch.empty_like(s["q"])
+    lse = torch.empty((9, 16), device="cuda")
+    ws = torch.full((c._ws_bytes,), 0xFF, dtype=torch.uint8, device="cuda")    # NaN everywhere
+    a = c.attend(1, s["q"], s["seq_lens"], prefix_len=400, out=out, lse=lse, workspace=ws)
+    assert a[0] is out and a[1] is lse
+    check(s, out, lse)
+    first = out.clone(), lse.clone()
+    for _ in range(10):
+        c.attend(1, s["q"], s["seq_lens"], prefix_len=400, out=out, lse=lse, workspace=ws)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])

@@ -1,0 +1,148 @@
+"""The operators together, and with the decode step: prefill a cache, attend over a shared prefix, score tokens."""
+import numpy as np
+import pytest
+import torch
+
+import fixtures as fx
+from fixtures.device import device_caches, device_model
+from tests.test_cache_append_gpu import rotate
+from tests.test_token_logprobs_gpu import check as check_scores
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_layer_over_a_shared_prompt():
+    """Prompt appended once, then steps of one token a sequence: append, attend, project, score; against 64 bits."""
+    import auto_regressive_decode_b200.mk as mk
+    g = torch.Generator("cuda").manual_seed(0)
+    B, nq, nkv, hd, page, P, steps, V = 5, 8, 2, 64, 16, 75, 3, 1000
+    max_ctx = P + steps
+    stride = -(-max_ctx // page)
+    # the prompt's whole pages belong to everyone; the page where it ends is each sequence's own
+    shared = P // page
+    pool = shared + B * (stride - shared)
+    order = torch.randperm(pool, generator=g, device="cuda").int()
+    table = torch.cat([order[:shared].expand(B, shared), order[shared:].view(B, -1)], 1).contiguous()
+    k, v = (torch.full((1, pool, nkv, page, hd), float("nan"), device="cuda").bfloat16() for _ in range(2))
+    cache = mk.Cache(k, v, n_q_heads=nq, batch=B, max_ctx=max_ctx, block_table=table, page_size=page)
+    qkv = torch.randn((P, nq + 2 * nkv, hd), generator=g, device="cuda")
+    starts = torch.tensor([0] + [P] * B, dtype=torch.int32, device="cuda")          # all of it is sequence 0's
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cache.append(0, qkv[:, nq:nq + nkv], qkv[:, nq + nkv:], zero, starts=starts)
+    bf = lambda t: t.bfloat16().double()  # noqa: E731
+    pos = torch.arange(P, device="cuda")
+    ks = [[bf(rotate(qkv[:, nq:nq + nkv], None, pos)[0])] for _ in range(B)]
+    vs = [[bf(qkv[:, nq + nkv:])] for _ in range(B)]
+    head = torch.randn((nq * hd, V), generator=g, device="cuda") * 0.05
+    for t in range(steps):
+        x = torch.randn((B, nq + 2 * nkv, hd), generator=g, device="cuda")
+        lens = torch.full((B,), P + t, dtype=torch.int32, device="cuda")
+        q = cache.append(0, x[:, nq:nq + nkv], x[:, nq + nkv:], lens, q=x[:, :nq])
+        out, lse = cache.attend(0, q, lens + 1, prefix_len=P)
+        logits = out.view(B, -1).float() @ head
+        tok = logits.argmax(-1).int()
+        check_scores(logits, tok, 5, mk.token_logprobs(logits, tok, top_k=5))
+        kk = bf(rotate(x[:, nq:nq + nkv], None, lens)[0])
+        for b in range(B):
+            ks[b].append(kk[b:b + 1])
+            vs[b].append(bf(x[b:b + 1, nq + nkv:]))
+            K, W = torch.cat(ks[b]).transpose(0, 1), torch.cat(vs[b]).transpose(0, 1)
+            a = torch.softmax(q[b].double().view(nkv, -1, hd) @ K.transpose(1, 2) * hd ** -0.5, -1)
+            o, size = a @ W, a @ W.abs()
+            err = (out[b].double().view(o.shape) - o).abs()
+            # the tolerance of the attention tests, and a half bf16 step for a key whose rounding falls on the other side
+            assert (err <= 2 ** -8 * (o.abs() + size) + 2 ** -8 * size).all()
+    assert cache.status() == mk.MK_OK
+
+
+@pytest.mark.parametrize("kw", [{}, {"batch": 3, "ffn_dim": 704, "ctx": 0, "ctx_lo": 5, "ctx_hi": 100}])
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_appended_through_the_decoders_cache_are_the_ones_it_attends(kw, paged):
+    import auto_regressive_decode_b200.mk as mk
+    cfg = fx.CONFIGS["tiny"].replace(**kw)
+    S0 = fx.context_lengths(cfg)
+    w = device_model(cfg)
+    kc, vc = device_caches(cfg, S0)
+    table, page = None, 0
+    if paged:
+        page = 256
+        stride = -(-cfg.max_ctx // page)
+        table = torch.arange(cfg.batch * stride, dtype=torch.int32, device="cuda").flip(0).view(cfg.batch, stride).contiguous()
+        shape = (cfg.n_layers, cfg.batch * stride, cfg.n_kv_heads, page, cfg.head_dim)
+    else:
+        shape = kc.shape
+    k2, v2 = torch.zeros(shape, dtype=torch.bfloat16, device="cuda"), torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    a = mk.Decoder(cfg, w, kc, vc)
+    b = mk.Decoder(cfg, w, k2, v2, block_table=table, page_size=page)
+    cache = b.cache()
+    # the same rows, appended in two calls at rotation position 0 (they count as rotated already)
+    for part in (0, 1):
+        counts = [int(s) // 2 if part == 0 else int(s) - int(s) // 2 for s in S0]
+        held = [0 if part == 0 else int(s) // 2 for s in S0]
+        starts = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+        lens = torch.tensor(held, dtype=torch.int32, device="cuda")
+        at = torch.zeros(sum(counts), dtype=torch.int32, device="cuda")
+        for layer in range(cfg.n_layers):
+            rows = [torch.cat([c[layer, i, :, h:h + n].transpose(0, 1) for i, (h, n) in enumerate(zip(held, counts))]) for c in (kc, vc)]
+            cache.append(layer, rows[0], rows[1], lens, starts=starts, positions=at)
+    assert cache.status() == mk.MK_OK
+    la, lb = (torch.empty((cfg.batch, cfg.vocab), dtype=torch.float32, device="cuda") for _ in range(2))
+    S = torch.from_numpy(S0.astype(np.int32)).cuda()
+    tok = torch.from_numpy(fx.tokens(cfg)[0].copy()).cuda()
+    a.step(tok, S, S, la)
+    b.step(tok, S, S, lb)
+    assert a.status() == mk.MK_OK and b.status() == mk.MK_OK
+    assert torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("kw", [{}, {"batch": 4, "ffn_dim": 704, "ctx": 0, "ctx_lo": 5, "ctx_hi": 100}])
+def test_scored_greedy_loop(kw):
+    """The picks of greedy(), and the scores of each step's logits."""
+    import auto_regressive_decode_b200.mk as mk
+    cfg = fx.CONFIGS["tiny"].replace(**kw)
+    steps = 6
+    S0 = fx.context_lengths(cfg)
+    w = device_model(cfg, gains="random")
+    tok = torch.from_numpy(fx.tokens(cfg)[0].copy()).cuda()
+    lens = torch.from_numpy(S0.astype(np.int32)).cuda()
+    runs = []
+    for scored in (False, True):
+        kc, vc = device_caches(cfg, S0)
+        dec = mk.Decoder(cfg, w, kc, vc)
+        picks = torch.empty((steps, cfg.batch), dtype=torch.int32, device="cuda")
+        if scored:
+            scores = dec.greedy_scored(steps, tok, lens, picks, top_k=4)
+        else:
+            last = torch.empty((cfg.batch, cfg.vocab), dtype=torch.float32, device="cuda")
+            dec.greedy(steps, tok, lens, picks, last)
+        assert dec.status() == mk.MK_OK
+        runs.append((picks, kc, vc))
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+    logprob, entropy, ids, tops, end = scores
+    assert torch.equal(end, lens + steps) and torch.equal(ids[:, :, 0], runs[0][0]) and torch.equal(tops[:, :, 0], logprob)
+    check_scores(last, picks[-1], 4, (logprob[-1], entropy[-1], ids[-1], tops[-1]))
+    # every step's scores are those of its logits, replayed on the picked tokens
+    kc, vc = device_caches(cfg, S0)
+    rep = mk.Decoder(cfg, w, kc, vc)
+    x = tok
+    for t in range(steps):
+        s = lens + t
+        rep.step(x, s, s, last)
+        check_scores(last, picks[t], 4, (logprob[t], entropy[t], ids[t], tops[t]))
+        x = picks[t].contiguous()
+    assert rep.status() == mk.MK_OK
+
+
+def test_scored_loop_that_runs_out_of_the_cache():
+    import auto_regressive_decode_b200.mk as mk
+    cfg = fx.CONFIGS["tiny"]
+    S0 = fx.context_lengths(cfg)
+    kc, vc = device_caches(cfg, S0)
+    dec = mk.Decoder(cfg, device_model(cfg), kc, vc)
+    steps = cfg.max_ctx - int(S0[0]) + 2
+    picks = torch.empty((steps, 1), dtype=torch.int32, device="cuda")
+    tok = torch.from_numpy(fx.tokens(cfg)[0].copy()).cuda()
+    logprob, _, _, _, _ = dec.greedy_scored(steps, tok, torch.from_numpy(S0.astype(np.int32)).cuda(), picks)
+    assert dec.status() == mk.MK_ERR_RANGE
+    assert (picks[-2:] == -1).all() and torch.isnan(logprob[-2:]).all() and torch.isfinite(logprob[:-2]).all()
