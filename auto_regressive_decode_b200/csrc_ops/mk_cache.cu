@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
 #include <new>
 
 #include "mk_cache.h"
@@ -47,13 +48,6 @@ __global__ void rope_table(float2* out, int T, int half, double theta) {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// The handle's device must be the current one: its pointers and the caller's stream belong to it.
-int on_device(const mk_cache* c) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MK_ERR_CUDA;
-  return dev == c->device ? MK_OK : MK_ERR_INVALID_ARG;
-}
-
 int launched(cudaError_t e) {
   if (e == cudaSuccess) return MK_OK;
   cudaGetLastError();
@@ -61,6 +55,25 @@ int launched(cudaError_t e) {
 }
 
 }  // namespace
+
+int current_sms() {
+  static std::atomic<int> known[64];  // an attribute of the device: the same for good
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 }  // namespace mk
 
 extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_cache** out) {
@@ -150,18 +163,19 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
 
 extern "C" int mk_cache_destroy(mk_cache* c) {
   if (!c) return MK_OK;
-  int dev = c->device, now = dev;
-  cudaGetDevice(&now);
-  if (now != dev) cudaSetDevice(dev);
-  const cudaError_t e = cudaFree(c->region);
-  if (now != dev) cudaSetDevice(now);
+  cudaError_t e;
+  {
+    mk::OnDevice here(c->device);
+    e = cudaFree(c->region);
+  }
   delete c;
   return mk::launched(e);
 }
 
 extern "C" int mk_cache_get_status(mk_cache* c, void* stream) {
   if (!c) return MK_ERR_INVALID_ARG;
-  if (int rc = mk::on_device(c)) return rc;
+  mk::OnDevice here(c->device);
+  if (!here.ok) return MK_ERR_CUDA;
   int st[2] = {0, 0};
   cudaStream_t s = (cudaStream_t)stream;
   if (cudaMemcpyAsync(st, c->view.status, sizeof(st), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
@@ -186,7 +200,8 @@ extern "C" int mk_cache_append(mk_cache* c, int layer, const mk_append_args* a, 
       !mk::aligned(a->q_norm, 16) || !mk::aligned(a->k_norm, 16) || !mk::aligned(a->starts, 4) ||
       !mk::aligned(a->seq_lens, 4) || !mk::aligned(a->positions, 4))
     return MK_ERR_UNSUPPORTED;
-  if (int rc = mk::on_device(c)) return rc;
+  mk::OnDevice here(c->device);
+  if (!here.ok) return MK_ERR_CUDA;
   return mk::launched(mk::append(*c, layer, *a, (cudaStream_t)stream));
 }
 
@@ -202,6 +217,7 @@ extern "C" int mk_cache_attend(mk_cache* c, int layer, const void* q, const int3
   if (!mk::aligned(q, 16) || !mk::aligned(out, 16) || !mk::aligned(seq_lens, 4) || !mk::aligned(lse, 4) ||
       !mk::aligned(workspace, 256))
     return MK_ERR_UNSUPPORTED;
-  if (int rc = mk::on_device(c)) return rc;
+  mk::OnDevice here(c->device);
+  if (!here.ok) return MK_ERR_CUDA;
   return mk::launched(mk::attend(*c, layer, q, seq_lens, prefix_len, scale, out, lse, workspace, (cudaStream_t)stream));
 }

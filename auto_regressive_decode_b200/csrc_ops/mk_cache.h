@@ -53,6 +53,29 @@ cudaError_t attend_prepare();
 cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* seq_lens, int prefix_len, float scale,
                    void* out, float* lse, void* workspace, cudaStream_t stream);
 
+// Makes `device` (-1: as it is) the current one of this thread for a scope.
+struct OnDevice {
+  int before = -1;
+  bool ok = true;
+  explicit OnDevice(int device) {
+    int now = -1;
+    if (device < 0) return;
+    ok = cudaGetDevice(&now) == cudaSuccess;
+    if (ok && now != device) {
+      ok = cudaSetDevice(device) == cudaSuccess;
+      if (ok) before = now;
+    }
+    if (!ok) cudaGetLastError();
+  }
+  ~OnDevice() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+  OnDevice(const OnDevice&) = delete;
+};
+
+// Streaming multiprocessors of the current device; 0 when it cannot be asked.
+int current_sms();
+
 }  // namespace mk
 
 struct mk_cache {

@@ -18,7 +18,7 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include "../../include/mk.h"
+#include "mk_cache.h"
 #include "mk_ptx.h"
 
 namespace mk {
@@ -339,7 +339,7 @@ __global__ void advance_lens(int32_t* lens, int n) {
 
 extern "C" int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_rows, int vocab,
                                  const int32_t* tokens, float* out_logprob, float* out_entropy, int top_k,
-                                 int32_t* out_top_ids, float* out_top_logprobs, void* stream) {
+                                 int32_t* out_top_ids, float* out_top_logprobs, int device, void* stream) {
   if (n_rows < 0 || vocab <= 0 || top_k < 0 || (dtype != MK_DTYPE_BF16 && dtype != MK_DTYPE_FP32))
     return MK_ERR_INVALID_ARG;
   if (n_rows == 0) return MK_OK;
@@ -350,12 +350,9 @@ extern "C" int mk_token_logprobs(const void* logits, int dtype, int64_t row_stri
       ((uintptr_t)tokens & 3) || ((uintptr_t)out_logprob & 3) || ((uintptr_t)out_entropy & 3) ||
       ((uintptr_t)out_top_ids & 3) || ((uintptr_t)out_top_logprobs & 3))
     return MK_ERR_UNSUPPORTED;
-  int dev = 0, n_sm = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
-  }
+  mk::OnDevice here(device);
+  const int n_sm = here.ok ? mk::current_sms() : 0;
+  if (!n_sm) return MK_ERR_CUDA;
   const mk::ScoreParams p{logits, row_stride, tokens, out_logprob, out_entropy, out_top_ids, out_top_logprobs, vocab, top_k};
   const cudaError_t e = es == 2 ? mk::score<uint16_t>(p, n_rows, n_sm, (cudaStream_t)stream)
                                 : mk::score<float>(p, n_rows, n_sm, (cudaStream_t)stream);
@@ -386,7 +383,7 @@ extern "C" int mk_decode_greedy_scored(mk_handle* h, const mk_model_desc* desc, 
       rc = mk_token_logprobs(logits, MK_DTYPE_FP32, desc->vocab, B, desc->vocab, picks, out_logprob + (size_t)t * B,
                              out_entropy ? out_entropy + (size_t)t * B : nullptr, top_k,
                              top_k ? out_top_ids + (size_t)t * B * top_k : nullptr,
-                             top_k ? out_top_logprobs + (size_t)t * B * top_k : nullptr, stream);
+                             top_k ? out_top_logprobs + (size_t)t * B * top_k : nullptr, -1, stream);
     if (rc != MK_OK) return rc;
     mk::advance_lens<<<1, 32, 0, s>>>(out_lens, B);
     if (cudaGetLastError() != cudaSuccess) return MK_ERR_CUDA;

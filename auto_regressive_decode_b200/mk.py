@@ -94,7 +94,7 @@ def _load():
         "mk_cache_append": (_i32, [H, _i32, ctypes.POINTER(mk_append_args), _P]),
         "mk_cache_attend": (_i32, [H, _i32, _P, _P, _i32, _f32, _P, _P, _P, ctypes.c_size_t, _P]),
         "mk_cache_attend_bytes": (ctypes.c_size_t, [H]),
-        "mk_token_logprobs": (_i32, [_P, _i32, ctypes.c_int64, _i32, _i32, _P, _P, _P, _i32, _P, _P, _P]),
+        "mk_token_logprobs": (_i32, [_P, _i32, ctypes.c_int64, _i32, _i32, _P, _P, _P, _i32, _P, _P, _i32, _P]),
         "mk_decode_greedy_scored": (_i32, [H, ctypes.POINTER(mk_model_desc), _i32, _P, _P, _P, _P, _P, _P, _P, _P, _i32,
                                            _P, _P]),
         "mk_plan_create": (_i32, [ctypes.POINTER(mk_model_desc), _i32, ctypes.POINTER(H)]),
@@ -343,22 +343,37 @@ class Decoder:
 
 # ---- operators on the KV cache, and scores of tokens ----------------------------------------------
 
-def _require(ok, what):
-    if not ok:
-        raise MkError(MK_ERR_INVALID_ARG, what)
+# The checks below build their messages only when they fail, and ask torch for the raw stream: a call on a
+# few tokens is as long as its host side.
+
+def _refuse(what):
+    raise MkError(MK_ERR_INVALID_ARG, what)
 
 
-def _dtype(t, what):
-    name = str(t.dtype)
-    _require(name in ("torch.bfloat16", "torch.float32"), f"{what}: bf16 or fp32 is wanted, got {name}")
-    return MK_DTYPE_BF16 if name == "torch.bfloat16" else MK_DTYPE_FP32
-
-
-def _int32(t, shape, device, what):
+def _float_dtype(t, what):
     import torch
-    _require(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == device and t.is_contiguous(),
-             f"{what}: a contiguous int32 tensor of shape {shape} on {device} is wanted")
-    return t.data_ptr()
+    if t.dtype is torch.bfloat16:
+        return MK_DTYPE_BF16
+    if t.dtype is torch.float32:
+        return MK_DTYPE_FP32
+    _refuse(f"{what}: bf16 or fp32 is wanted, got {t.dtype}")
+
+
+def _raw_stream(index, stream):
+    """cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _empty(shape, dtype, device, stream):
+    """Uninitialised tensor of the stream that is going to write it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class Cache:
@@ -367,28 +382,30 @@ class Cache:
     k, v: device bf16 [L][B][n_kv][max_ctx][hd], or with block_table (device int32
     [B][ceil(max_ctx/page_size)]) page pools [L][n_pages][n_kv][page_size][hd]; page_size a multiple of 16.
     Calls are asynchronous; tensors must stay alive until the stream has used them, and they and the stream
-    belong to the cache's device."""
+    belong to the cache's device, which need not be the current one."""
 
     def __init__(self, k, v, n_q_heads, batch, max_ctx, block_table=None, page_size=0, rope_theta=1e4, rms_eps=1e-6):
         import torch
         self.torch = torch
-        _require(k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.dim() == 5 and k.is_cuda and
-                 v.device == k.device and k.is_contiguous() and v.is_contiguous(),
-                 "Cache: k and v are contiguous bf16 device tensors of one shape [.][.][.][.][.]")
+        if not (k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.dim() == 5 and k.is_cuda and
+                v.device == k.device and k.is_contiguous() and v.is_contiguous()):
+            _refuse("Cache: k and v are contiguous bf16 device tensors of one shape [.][.][.][.][.]")
         L, n, nkv, rows, hd = k.shape
-        self.device = k.device
-        table = None
-        if block_table is None:
-            _require(n == batch and rows == max_ctx, f"Cache: k of shape [L][{batch}][n_kv][{max_ctx}][hd] is wanted")
-            kv = mk_kv(k.data_ptr(), v.data_ptr(), None, 0, 0)
-        else:
-            _require(rows == page_size > 0, f"Cache: k of shape [L][n_pages][n_kv][{page_size}][hd] is wanted")
-            table = _int32(block_table, (batch, -(-max_ctx // page_size)), k.device, "Cache: block_table")
-            kv = mk_kv(k.data_ptr(), v.data_ptr(), table, page_size, n)
-        self._keep = (k, v, block_table)
+        self.device, self._index = k.device, k.device.index
         self.n_layers, self.batch, self.max_ctx = L, batch, max_ctx
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, nkv, hd
-        self._q_shape = (batch, n_q_heads, hd)
+        self._q_shape, self._lse_shape = (batch, n_q_heads, hd), (batch, n_q_heads)
+        self._lens_shape, self._starts_shape = (batch,), (batch + 1,)
+        if block_table is None:
+            if n != batch or rows != max_ctx:
+                _refuse(f"Cache: k of shape [L][{batch}][n_kv][{max_ctx}][hd] is wanted")
+            kv = mk_kv(k.data_ptr(), v.data_ptr(), None, 0, 0)
+        else:
+            if rows != page_size or page_size <= 0:
+                _refuse(f"Cache: k of shape [L][n_pages][n_kv][{page_size}][hd] is wanted")
+            table = self._ints(block_table, (batch, -(-max_ctx // page_size)), "Cache: block_table")
+            kv = mk_kv(k.data_ptr(), v.data_ptr(), table, page_size, n)
+        self._keep = (k, v, block_table)
         desc = mk_cache_desc(L, batch, n_q_heads, nkv, hd, max_ctx, rms_eps, rope_theta)
         h = _P()
         with torch.cuda.device(self.device):
@@ -396,50 +413,56 @@ class Cache:
         self.h = h
         self._ws_bytes = mk_cache_attend_bytes(h)
 
-    def _rows(self, t, n, heads, dtype, what):
+    def _ints(self, t, shape, what):
+        if t.dtype is self.torch.int32 and t.shape == shape and t.device == self.device and t.is_contiguous():
+            return t.data_ptr()
+        _refuse(f"{what}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
+
+    def _buffer(self, t, shape, dtype, what):
+        if t.dtype is dtype and t.shape == shape and t.device == self.device and t.is_contiguous():
+            return t.data_ptr()
+        _refuse(f"{what}: a contiguous tensor of shape {tuple(shape)}, {dtype}, on {self.device} is wanted")
+
+    def _rows(self, t, shape, dtype, what):
         """Pointer and token stride of [n][heads][hd] whose heads are contiguous within a token."""
-        hd = self.head_dim
-        _require(t.shape == (n, heads, hd) and t.dtype == dtype and t.device == self.device and
-                 (t.stride(2) == 1 and (t.stride(1) == hd or heads == 1) or n == 0),
-                 f"append: {what} of shape ({n}, {heads}, {hd}), {dtype}, heads contiguous, on {self.device} is wanted")
-        return t.data_ptr(), t.stride(0)
+        if t.shape == shape and t.dtype is dtype and t.device == self.device:
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == shape[2] or shape[1] == 1) or shape[0] == 0:
+                return t.data_ptr(), s0
+        _refuse(f"append: {what} of shape {shape}, {dtype}, heads contiguous, on {self.device} is wanted")
 
     def append(self, layer, k, v, seq_lens, q=None, starts=None, positions=None, q_norm=None, k_norm=None, q_out=None,
                stream=None):
         """Append keys and values (bf16 or fp32 [n][n_kv][hd]) to the cache, the keys rotated; returns the rotated
         q (bf16 [n][n_q][hd]) where q is given.  seq_lens int32 [B]: rows held before; starts int32 [B + 1]: the
         tokens of each sequence (None: one each); see mk_cache_append."""
-        torch, dev = self.torch, self.device
-        st = stream or torch.cuda.current_stream(dev)
-        n = k.shape[0]
-        dt = _dtype(k, "append")
-        a = mk_append_args()
-        a.k, a.k_stride = self._rows(k, n, self.n_kv_heads, k.dtype, "k")
-        a.v, a.v_stride = self._rows(v, n, self.n_kv_heads, k.dtype, "v")
+        bf16, hd = self.torch.bfloat16, self.head_dim
+        n, dt = k.shape[0], k.dtype
+        code = _float_dtype(k, "append")
+        kv_shape = (n, self.n_kv_heads, hd)
+        kp, ks = self._rows(k, kv_shape, dt, "k")
+        vp, vs = self._rows(v, kv_shape, dt, "v")
+        qp = qs = qop = 0
         if q is not None:
-            a.q, a.q_stride = self._rows(q, n, self.n_q_heads, k.dtype, "q")
+            q_shape = (n, self.n_q_heads, hd)
+            qp, qs = self._rows(q, q_shape, dt, "q")
             if q_out is None:
-                with torch.cuda.stream(st):
-                    q_out = torch.empty((n, self.n_q_heads, self.head_dim), dtype=torch.bfloat16, device=dev)
-            _require(q_out.shape == q.shape and q_out.dtype == torch.bfloat16 and q_out.device == dev and
-                     q_out.is_contiguous(), "append: q_out")
-            a.q_out = q_out.data_ptr()
-        else:
-            _require(q_out is None, "append: q_out without q")
-        if starts is not None:
-            a.starts = _int32(starts, (self.batch + 1,), dev, "append: starts")
-        else:
-            _require(n == self.batch, f"append: {self.batch} tokens are wanted without starts")
-        a.seq_lens = _int32(seq_lens, (self.batch,), dev, "append: seq_lens")
-        if positions is not None:
-            a.positions = _int32(positions, (n,), dev, "append: positions")
-        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if g is not None:
-                _require(g.shape == (self.head_dim,) and g.dtype == torch.bfloat16 and g.device == dev and
-                         g.is_contiguous(), f"append: {name}")
-                setattr(a, name, g.data_ptr())
-        a.n_tokens, a.dtype = n, dt
-        self._call(mk_cache_append, "mk_cache_append", layer, ctypes.byref(a), st.cuda_stream)
+                q_out = _empty(q_shape, bf16, self.device, stream)
+                qop = q_out.data_ptr()
+            else:
+                qop = self._buffer(q_out, q_shape, bf16, "append: q_out")
+        elif q_out is not None:
+            _refuse("append: q_out without q")
+        if starts is None and n != self.batch:
+            _refuse(f"append: {self.batch} tokens are wanted without starts")
+        a = mk_append_args(
+            qp, kp, vp, qs, ks, vs,
+            None if starts is None else self._ints(starts, self._starts_shape, "append: starts"),
+            self._ints(seq_lens, self._lens_shape, "append: seq_lens"),
+            None if positions is None else self._ints(positions, (n,), "append: positions"),
+            None if q_norm is None else self._buffer(q_norm, (hd,), bf16, "append: q_norm"),
+            None if k_norm is None else self._buffer(k_norm, (hd,), bf16, "append: k_norm"), qop, n, code)
+        check(mk_cache_append(self.h, layer, a, _raw_stream(self._index, stream)), "mk_cache_append")
         return q_out
 
     def attend(self, layer, q, seq_lens, prefix_len=0, scale=0.0, out=None, lse=None, workspace=None, stream=None):
@@ -447,34 +470,25 @@ class Cache:
         below prefix_len are sequence 0's for all.  Returns (out bf16 [B][n_q][hd], lse fp32 [B][n_q]); see
         mk_cache_attend."""
         torch, dev, shape = self.torch, self.device, self._q_shape
-        st = stream or torch.cuda.current_stream(dev)
-        _require(q.shape == shape and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous(),
-                 f"attend: a contiguous bf16 q of shape {shape} on {dev} is wanted")
-        lens = _int32(seq_lens, (self.batch,), dev, "attend: seq_lens")
-        if out is None or lse is None or workspace is None:
-            with torch.cuda.stream(st):
-                out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
-                lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
-                if workspace is None:
-                    workspace = torch.empty((self._ws_bytes,), dtype=torch.uint8, device=dev)
-        _require(out.shape == shape and out.dtype == torch.bfloat16 and out.device == dev and out.is_contiguous() and
-                 lse.shape == shape[:2] and lse.dtype == torch.float32 and lse.device == dev and lse.is_contiguous() and
-                 workspace.device == dev and workspace.is_contiguous(), "attend: out, lse, workspace")
-        self._call(mk_cache_attend, "mk_cache_attend", layer, q.data_ptr(), lens, prefix_len, scale, out.data_ptr(),
-                   lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
+        qp = self._buffer(q, shape, torch.bfloat16, "attend: q")
+        lens = self._ints(seq_lens, self._lens_shape, "attend: seq_lens")
+        if out is None:
+            out = _empty(shape, torch.bfloat16, dev, stream)
+        if lse is None:
+            lse = _empty(self._lse_shape, torch.float32, dev, stream)
+        if workspace is None:
+            workspace = _empty(self._ws_bytes, torch.uint8, dev, stream)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            _refuse(f"attend: a contiguous workspace on {dev} is wanted")
+        check(mk_cache_attend(self.h, layer, qp, lens, prefix_len, scale,
+                              self._buffer(out, shape, torch.bfloat16, "attend: out"),
+                              self._buffer(lse, self._lse_shape, torch.float32, "attend: lse"), workspace.data_ptr(),
+                              workspace.nbytes, _raw_stream(self._index, stream)), "mk_cache_attend")
         return out, lse
-
-    def _call(self, fn, name, *args):
-        torch = self.torch
-        if torch.cuda.current_device() == self.device.index:
-            return check(fn(self.h, *args), name)
-        with torch.cuda.device(self.device):
-            return check(fn(self.h, *args), name)
 
     def status(self, stream=None):
         """First error recorded on the device since the last call (synchronises the stream)."""
-        with self.torch.cuda.device(self.device):
-            return mk_cache_get_status(self.h, (stream or self.torch.cuda.current_stream()).cuda_stream)
+        return mk_cache_get_status(self.h, _raw_stream(self._index, stream))
 
     def close(self):
         if getattr(self, "h", None):
@@ -492,21 +506,19 @@ def token_logprobs(logits, tokens, top_k=0, stream=None):
     """Scores of tokens (int32 [n]) under logits (bf16 or fp32 [n][vocab], rows any stride apart): (logprob fp32
     [n], entropy fp32 [n], ids int32 [n][top_k], their log probabilities fp32 [n][top_k]); see mk_token_logprobs."""
     import torch
-    _require(logits.dim() == 2 and logits.is_cuda and (logits.stride(1) == 1 or logits.shape[1] == 1),
-             "token_logprobs: device logits [n][vocab] with contiguous rows are wanted")
-    dt, dev, (n, V) = _dtype(logits, "token_logprobs"), logits.device, logits.shape
-    st = stream or torch.cuda.current_stream(dev)
-    tok = _int32(tokens, (n,), dev, "token_logprobs: tokens")
-    _require(0 <= top_k <= 32, "token_logprobs: top_k 0..32 is wanted")
-    with torch.cuda.stream(st):
-        scores = torch.empty((2, n), dtype=torch.float32, device=dev)
-        ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
-        tops = torch.empty((n, top_k), dtype=torch.float32, device=dev)
-    logprob, entropy = scores[0], scores[1]
-    args = (logits.data_ptr(), dt, logits.stride(0), n, V, tok, logprob.data_ptr(), entropy.data_ptr(), top_k,
-            ids.data_ptr(), tops.data_ptr(), st.cuda_stream)
-    with torch.cuda.device(dev):
-        check(mk_token_logprobs(*args), "mk_token_logprobs")
+    if not (logits.is_cuda and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)):
+        _refuse("token_logprobs: device logits [n][vocab] with contiguous rows are wanted")
+    code, dev, (n, V) = _float_dtype(logits, "token_logprobs"), logits.device, logits.shape
+    if not (tokens.dtype is torch.int32 and tokens.shape == (n,) and tokens.device == dev and tokens.is_contiguous()):
+        _refuse(f"token_logprobs: contiguous int32 tokens of shape ({n},) on {dev} are wanted")
+    if not 0 <= top_k <= 32:
+        _refuse("token_logprobs: top_k 0..32 is wanted")
+    logprob, entropy = _empty((2, n), torch.float32, dev, stream).unbind(0)
+    ids = _empty((n, top_k), torch.int32, dev, stream)
+    tops = _empty((n, top_k), torch.float32, dev, stream)
+    check(mk_token_logprobs(logits.data_ptr(), code, logits.stride(0), n, V, tokens.data_ptr(), logprob.data_ptr(),
+                            entropy.data_ptr(), top_k, ids.data_ptr(), tops.data_ptr(), dev.index,
+                            _raw_stream(dev.index, stream)), "mk_token_logprobs")
     return logprob, entropy, ids, tops
 
 

@@ -230,7 +230,9 @@ int mk_decode_step_noalloc(const mk_model_desc* desc, const mk_weights* weights,
  *
  * A cache handle describes a cache (the same layouts as mk_kv; page_size is a
  * multiple of 16 here) and holds its rotation table and tensor maps.  It may
- * describe the cache of an mk_handle.  The calls only read it, so calls on
+ * describe the cache of an mk_handle.  It belongs to the device that was
+ * current at mk_cache_create; the calls run there, whichever device is current, and
+ * restore the current one.  The calls only read it, so calls on
  * several streams may overlap as far as their buffers allow: an attend reads
  * what an earlier append of the same stream wrote, and overlapping attends
  * need a workspace each.
@@ -329,6 +331,7 @@ size_t mk_cache_attend_bytes(const mk_cache* c);
  *   out_top_ids, out_top_logprobs  device int32 / fp32 [n_rows][top_k], best
  *             first, the lower id first among equal logits; top_k 0..32
  *             (NULL when 0)
+ *   device    of the pointers and the stream; -1: the current one
  * Logits of -infinity have probability 0 and are no alternatives: missing
  * alternatives are id -1, log probability -infinity.  A row that holds a NaN
  * or +infinity, or nothing but -infinity, has no distribution: its scores are
@@ -336,7 +339,7 @@ size_t mk_cache_attend_bytes(const mk_cache* c);
  */
 int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_rows, int vocab, const int32_t* tokens,
                       float* out_logprob, float* out_entropy, int top_k, int32_t* out_top_ids,
-                      float* out_top_logprobs, void* stream);
+                      float* out_top_logprobs, int device, void* stream);
 
 /*
  * mk_decode_greedy with the scores of every picked token, mk_token_logprobs of

@@ -52,7 +52,7 @@ def test_null_arguments():
 
 
 def scores(logits=FAKE, dtype=mk.MK_DTYPE_FP32, stride=10, rows=1, vocab=10, tokens=FAKE, logprob=FAKE, entropy=FAKE, k=2, ids=FAKE, tops=FAKE):
-    return mk.mk_token_logprobs(logits, dtype, stride, rows, vocab, tokens, logprob, entropy, k, ids, tops, None)
+    return mk.mk_token_logprobs(logits, dtype, stride, rows, vocab, tokens, logprob, entropy, k, ids, tops, -1, None)
 
 
 @pytest.mark.parametrize("kw,rc", [
