@@ -70,6 +70,13 @@ __device__ __forceinline__ void tma_box2(uint32_t dst, const void* map, int c0, 
       : "memory");
 }
 
+// `bytes` contiguous bytes (16-byte aligned at both ends, a multiple of 16) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // ---- programmatic dependent launch ---------------------------------------------------
 // Wait until every grid that this one depends on has finished and its writes are visible.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

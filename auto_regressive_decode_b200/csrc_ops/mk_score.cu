@@ -1,10 +1,10 @@
 // Log probabilities of given tokens, entropy and the most likely alternatives.
 //
-// One pass over a row of logits x.  Every thread keeps its maximum m and, in
-// units of log2 (d = (x - m) log2 e), z = sum 2^d and s = sum 2^d d, moved to a
-// new m when it grows; the threads' (m, z, s) join at the end:
+// One pass over a row of logits x.  Every thread keeps a reference m near its
+// maximum and, in units of log2 (d = (x - m) log2 e), z = sum 2^d and
+// s = sum 2^d d; the threads' (m, z, s) move to the largest m at the end:
 //   logprob(t) = x_t - m - ln z,   entropy = ln z - ln 2 * s / z
-// (every term of the entropy is >= 0: nothing cancels).
+// (terms of one sign but for the few above the reference: nothing cancels).
 //
 // Alternatives: a key packs the order-preserving map of the logit over the
 // inverted index, so that the largest key is the largest logit, of the lowest
@@ -18,6 +18,9 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "mk_cache.h"
 #include "mk_ptx.h"
 
@@ -28,8 +31,7 @@ using namespace ptx;
 namespace cg = cooperative_groups;
 
 constexpr int kMaxTop = 32;
-constexpr int kCap = 1024;    // candidate buffer
-constexpr int kChunk = 16;    // logits a thread holds at once
+constexpr int kVecs = 4;      // 16-byte vectors of logits a thread holds at once
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 typedef unsigned long long Key;
 
@@ -40,7 +42,7 @@ struct ScoreParams {
   float *logprob, *entropy;
   int32_t* ids;
   float* tops;
-  int vocab, top_k;
+  int vocab, top_k, rows;
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -60,257 +62,488 @@ __device__ __forceinline__ Key make_key(float x, int i) { return ((Key)ordered(x
 // Running maximum, sum and weighted sum (log2 units).
 struct Sum {
   float m, z, s;
-  __device__ __forceinline__ void join(const Sum& o) {
-    const float M = fmaxf(m, o.m), ref = M == -INFINITY ? 0.f : M;
-    auto part = [&](const Sum& x, float& zz, float& ss) {
-      if (x.z == 0.f) return;  // nothing but -infinity (a NaN sum is passed on)
-      const float dm = (x.m - ref) * kLog2e, f = ex2(dm);
-      zz += f * x.z;
-      if (f > 0.f) ss += f * (x.s + x.z * dm);
-    };
-    float zz = 0.f, ss = 0.f;
-    part(*this, zz, ss);
-    part(o, zz, ss);
-    m = M;
-    z = zz;
-    s = ss;
+};
+
+// Two fp32 values in one register pair (sm_100 add / mul / fma.rn.f32x2).
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The logits of one 16-byte vector, and their maximum (NaN ignored).
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kLen = 4;
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+  static __device__ __forceinline__ float one(float x) { return x; }
+  static __device__ __forceinline__ void get(const uint4& r, float f[4]) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y); f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ float top(const uint4 (&r)[kVecs]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      float f[4];
+      get(r[u], f);
+      m = fmaxf(fmaxf(m, fmaxf(f[0], f[1])), fmaxf(f[2], f[3]));
+    }
+    return m;
+  }
+};
+template <>
+struct Vec<uint16_t> {
+  static constexpr int kLen = 8;
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+  static __device__ __forceinline__ void get(const uint4& r, float f[8]) {
+    f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
+    f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float top(const uint4 (&r)[kVecs]) {
+    uint32_t m = 0xff80ff80u;  // -infinity twice
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) m = max2(max2(m, max2(r[u].x, r[u].y)), max2(r[u].z, r[u].w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
   }
 };
 
-template <typename T>
-struct Load;  // 16 consecutive logits a thread, in 16-byte vectors a warp apart
-template <>
-struct Load<float> {
-  static constexpr int kVec = 4;
-};
-template <>
-struct Load<uint16_t> {
-  static constexpr int kVec = 8;
-};
+constexpr int kStagesS = 4;   // chunks in flight, each NT * kVecs vectors
+constexpr int kGroups = 64;   // thread groups whose maxima raise the limit
+constexpr int kRoom = 64;     // keys a warp holds
 
+// NT compute threads and a producer warp.
 template <int NT>
 struct Shared {
-  Key buf[kCap];
+  static constexpr int kWarps = NT / 32, kStageBytes = NT * kVecs * 16;
+  uint8_t ring[kStagesS][kStageBytes];
+  unsigned long long full[kStagesS], empty[kStagesS];
+  alignas(16) Key keys[kWarps * kRoom];  // each warp's, then all of them side by side
   Key best[kMaxTop];
-  Key limit;  // keys below it are not among the best
-  int count;
-  Sum part[NT / 32];
-  Sum sum;    // this block's
-  int n_best;
+  alignas(16) uint32_t tops[kGroups];
+  uint32_t raised, hint;    // upper words of limits: from the groups' maxima, and the highest that a warp found by itself
+  int held[kWarps];
+  int n_best, dead;
+  Sum part[kWarps];
+  Sum sum;                  // this block's
 };
 
-// The n keys of buf: the k largest to best[], in order.  Returns how many.
+// The NT compute threads.
 template <int NT>
-__device__ __forceinline__ int select_best(Shared<NT>& sh, int n, int k) {
-  for (int e = threadIdx.x; e < n; e += NT) {
-    const Key x = sh.buf[e];
-    int rank = 0;
-    for (int i = 0; i < n; ++i) rank += sh.buf[i] > x;
-    if (rank < k) sh.best[rank] = x;
-  }
-  __syncthreads();
-  return min(n, k);
+__device__ __forceinline__ void compute_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
 }
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT) score_kernel(const __grid_constant__ ScoreParams p) {
-  constexpr int VEC = Load<T>::kVec, U = kChunk / VEC;
-  __shared__ Shared<NT> sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int parts = cluster.num_blocks(), part = cluster.block_rank();
-  const int tid = threadIdx.x, k = p.top_k;
-  const int64_t row = blockIdx.x / parts;
-  const T* x = reinterpret_cast<const T*>(p.logits) + row * p.stride;
-
-  // this block's logits [c0, c1), walked in aligned vectors: vector v covers
-  // [v * VEC - skew, ...) where skew is the row's offset from alignment
-  const int skew = (int)(((uintptr_t)x & 15) / sizeof(T));
-  const int vecs = (p.vocab + skew + VEC - 1) / VEC;
-  const int v0 = (int)((int64_t)vecs * part / parts), v1 = (int)((int64_t)vecs * (part + 1) / parts);
-
-  if (tid == 0) {
-    sh.limit = 0;
-    sh.count = 0;
+// Largest k of the n keys at `keys`, sorted, to `best` (not `keys` itself), by
+// comparison with all; threads t of nt (whole warps), n <= 2 nt.
+__device__ __forceinline__ void rank_keys(const Key* keys, int n, int k, Key* best, int t, int nt) {
+  for (; (t & ~31) < n; t += nt) {
+    const Key a = t < n ? keys[t] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i + 1 < n; i += 2) {
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(keys + i);
+      rank += (q.x > a) + (q.y > a);
+    }
+    if (n & 1) rank += keys[n - 1] > a;
+    if (t < n && rank < k) best[rank] = a;
   }
-  Sum a{-INFINITY, 0.f, 0.f};
+}
 
-  uint4 raw[U];
-  auto fetch = [&](int base) {  // vectors base + tid, base + NT + tid, ...
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = base + u * NT + tid;
-      const int i0 = v * VEC - skew;
-      if (v < v1 && i0 >= 0 && i0 + VEC <= p.vocab) {
-        raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + i0));
-      } else {  // the ends of the row: nothing outside of it is read
-        T e[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const bool in = v < v1 && i0 + i >= 0 && i0 + i < p.vocab;
-          if constexpr (sizeof(T) == 4) e[i] = in ? x[i0 + i] : -INFINITY;
-          else e[i] = in ? x[i0 + i] : (T)0xff80;
-        }
-        memcpy(&raw[u], e, 16);
-      }
-    }
-  };
-  fetch(v0);
-  __syncthreads();
-  for (int base = v0; base < v1; base += NT * U) {
-    float f[kChunk];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          f[u * 4 + i] = __uint_as_float(w[i]);
-        } else {
-          f[u * 8 + 2 * i] = bf16_lo(w[i]);
-          f[u * 8 + 2 * i + 1] = bf16_hi(w[i]);
-        }
-      }
-    }
-    if (base + NT * U < v1) fetch(base + NT * U);
-    float top = f[0];
-#pragma unroll
-    for (int i = 1; i < kChunk; ++i) top = fmaxf(top, f[i]);
-    if (top > a.m) {
-      if (a.m > -INFINITY) {
-        const float dm = (a.m - top) * kLog2e, g = ex2(dm);
-        a.s = g > 0.f ? g * (a.s + a.z * dm) : 0.f;
-        a.z *= g;
-      }
-      a.m = top;
-    }
-    const float ref = a.m == -INFINITY ? 0.f : a.m;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      // far below the maximum 2^d is 0: the bound keeps 0 * -infinity out of s
-      const float d = max_nan((f[i] - ref) * kLog2e, -150.f), e = ex2(d);
-      a.z += e;
-      a.s = fmaf(e, d, a.s);
-    }
-    if (k > 0) {
-      const uint32_t lim = (uint32_t)(sh.limit >> 32);
-      const uint32_t mine = ordered(top);
-      const bool cand = top > -INFINITY && mine >= lim;
-      const int n = __syncthreads_count(cand);
-      if (n) {
-        if (n > 2 * k) {  // raise the threshold: the largest 16-bit prefix that k thread maxima reach
-          uint32_t t = 0;
-          for (int bit = 15; bit >= 0; --bit) {
-            const uint32_t want = t | (1u << bit);
-            if (__syncthreads_count(cand && (mine >> 16) >= want) >= k) t = want;
-          }
-          if (tid == 0 && ((Key)t << 48) > sh.limit) sh.limit = (Key)t << 48;
-          __syncthreads();
-        }
-        uint32_t todo = cand ? 0xffffu : 0u;
-        while (true) {
-          const Key limit = sh.limit;
-          if (todo) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-              if (todo >> i & 1) {
-                const int idx = (base + (i / VEC) * NT + tid) * VEC - skew + i % VEC;
-                const Key key = make_key(f[i], idx);
-                bool left = false;
-                if (f[i] > -INFINITY && key >= limit) {
-                  const int at = atomicAdd(&sh.count, 1);
-                  if (at < kCap) sh.buf[at] = key;
-                  else left = true;
-                }
-                if (!left) todo &= ~(1u << i);
-              }
-            }
-          }
-          __syncthreads();
-          const bool full = sh.count > kCap;
-          if (!full) break;
-          select_best<NT>(sh, kCap, k);
-          if (tid < k) sh.buf[tid] = sh.best[tid];
-          if (tid == 0) {
-            sh.count = k;
-            sh.limit = sh.best[k - 1] + 1;
-          }
-          __syncthreads();
-        }
-      }
+// The block's part of a row, walked in aligned vectors: vector v covers logits
+// from v * VEC - skew on, where skew is the row's offset from alignment.  Whole
+// vectors [v0, v1) come through the ring in chunks; the partial ones at the
+// row's ends are read by themselves (nothing outside the row is read).
+template <typename T>
+struct Part {
+  const T* x;
+  int skew, v0, v1;
+  __device__ __forceinline__ Part(const ScoreParams& p, int row, int part, int parts) {
+    constexpr int VEC = Vec<T>::kLen;
+    x = reinterpret_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+    skew = (int)(((uintptr_t)x & 15) / sizeof(T));
+    v0 = skew ? 1 : 0;
+    v1 = max((p.vocab + skew) / VEC, v0);
+    if (parts > 1) {
+      const int n = v1 - v0, first = v0;
+      v0 = first + (int)((int64_t)n * part / parts);
+      v1 = first + (int)((int64_t)n * (part + 1) / parts);
     }
   }
+};
 
-  // join the threads' sums
+// A thread's sums.  d = x log2 e - c is one fma, c = m log2 e rounded; what the
+// rounding left (res) is put right when the sums move to another reference.
+struct Acc {
+  float m = -INFINITY, c = 0.f, res = 0.f, z = 0.f, s = 0.f;
+  bool huge = false;  // m log2 e overflows, or its rounding is no small part of a power of two
+  // Sums to the reference whose c is `dm` below this one's.
+  __device__ __forceinline__ void move(float dm) {
+    if (z == 0.f) return;  // nothing but -infinity so far (a NaN sum is passed on)
+    const float f = ex2(dm);
+    s = f > 0.f ? f * (s + z * dm) : 0.f;
+    z *= f;
+  }
+  // A new reference; the next one comes when a logit is kSlack above it: 2^d
+  // and its sums stay far inside fp32, so that few chunks move the sums.
+  static constexpr float kSlack = 16.f;
+  __device__ __noinline__ void lift(float top, float& lifted) {
+    const float m0 = m, res0 = res;
+    m = top;
+    huge = fabsf(top) > 1e6f;
+    c = huge ? 0.f : top * kLog2e;
+    res = huge ? 0.f : fmaf(top, kLog2e, -c);
+    move(m0 == -INFINITY ? 0.f : (m0 - top) * kLog2e - res0 + res);
+    lifted = top + kSlack;
+  }
+  __device__ __forceinline__ Sum sum() {
+    move(-res);
+    return Sum{m, z, s};
+  }
+};
+
+// Sum of the 32 lanes, in every lane.
+__device__ __forceinline__ Sum warp_join(Sum a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  Sum r{m, 0.f, 0.f};
+  if (a.z != 0.f) {  // else nothing but -infinity (a NaN sum is passed on)
+    const float dm = (a.m - (m == -INFINITY ? 0.f : m)) * kLog2e, f = ex2(dm);
+    r.z = f * a.z;
+    r.s = f > 0.f ? f * (a.s + a.z * dm) : 0.f;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    Sum b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.z = __shfl_xor_sync(0xffffffffu, a.z, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    a.join(b);
+    r.z += __shfl_xor_sync(0xffffffffu, r.z, o);
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
   }
-  if (tid % 32 == 0) sh.part[tid / 32] = a;
-  __syncthreads();
+  return r;
+}
+
+// Rows of a cluster of `parts` blocks; with one block a row, blocks step over the rows.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int VEC = Vec<T>::kLen, U = kVecs, CH = NT * U;
+  using S = Shared<NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  S& sh = *reinterpret_cast<S*>(smem);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k = p.top_k;
+  const int row0 = blockIdx.x / parts, row_step = gridDim.x / parts;
+  volatile int* dead = &sh.dead;
+
   if (tid == 0) {
-    for (int w = 1; w < NT / 32; ++w) a.join(sh.part[w]);
-    sh.sum = a;
+    for (int i = 0; i < kStagesS; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), S::kWarps);
+    }
+    sh.dead = 0;
+    fence_mbar_init();
   }
-  const int got = k > 0 ? select_best<NT>(sh, sh.count, k) : 0;
-  if (tid == 0) sh.n_best = got;
   __syncthreads();
 
-  if (parts > 1) {
-    cluster.sync();
-    if (part == 0) {
-      if (tid == 0)
-        for (int r = 1; r < parts; ++r) a.join(cluster.map_shared_rank(&sh, r)->sum);
-      // the blocks' best keys, one after another
-      int n = got;
-      if (tid < got) sh.buf[tid] = sh.best[tid];
-      for (int r = 1; r < parts; ++r) {
-        const Shared<NT>* o = cluster.map_shared_rank(&sh, r);
-        const int m = o->n_best;
-        if (tid < m) sh.buf[n + tid] = o->best[tid];
-        n += m;
+  if (warp == S::kWarps) {  // ---- producer: the chunks of all rows, as far ahead as the ring goes
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int row = row0; row < p.rows; row += row_step) {
+        const Part<T> r(p, row, part, parts);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(r.x - r.skew);
+        for (int v = r.v0; v < r.v1; v += CH) {
+          const uint32_t bytes = min(CH, r.v1 - v) * 16;
+          mbar_wait(smem_addr(&sh.empty[slot]), phase ^ 1, dead);
+          if (!*dead) {
+            mbar_expect_tx(smem_addr(&sh.full[slot]), bytes);
+            bulk_load(smem_addr(sh.ring[slot]), src + (int64_t)v * 16, bytes, smem_addr(&sh.full[slot]));
+          }
+          if (++slot == kStagesS) slot = 0, phase ^= 1;
+        }
       }
-      __syncthreads();
-      if (tid == 0) sh.sum = a;
+      if (*dead) {  // copies still in flight land before the block's shared memory is given back
+        const uint64_t t0 = globaltimer();
+        for (int i = 0; i < kStagesS; ++i)
+          while (!mbar_try(smem_addr(&sh.full[i]), i < slot ? phase : phase ^ 1) && globaltimer() - t0 < 10000000ull) {
+          }
+      }
+    }
+    __syncwarp();
+    if (parts > 1) {
+      cluster.sync();
+      cluster.sync();
+    }
+    return;
+  }
+
+  Key* mine = sh.keys + warp * kRoom;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int row = row0; row < p.rows; row += row_step) {
+    const Part<T> r(p, row, part, parts);
+    Acc acc;
+    float most = -INFINITY, lifted = -INFINITY;  // the largest logit so far; what the next reference has to exceed
+    Key limit = 0;             // keys below it are not among the best,
+    float least = -3.402823466e38f;  // nor are logits below this one
+    auto set_limit = [&](Key to) {
+      if (to > limit) {
+        limit = to;
+        least = from_ordered((uint32_t)(to >> 32));
+      }
+    };
+    int held = 0;   // keys of this warp
+    float given = NAN;
+    if (tid == 0 && part == 0) {
+      const int t = __ldg(p.tokens + row);
+      if (t >= 0 && t < p.vocab) given = Vec<T>::one(r.x[t]);
+    }
+    if (tid == 0) sh.hint = 0;
+    // the keys of a warp, a lane each (0: none), into its room; a full room is cut to its k best
+    auto push = [&](Key key) {
+      const bool pass = key != 0 && key >= limit;
+      const uint32_t who = __ballot_sync(0xffffffffu, pass);
+      const int n = __popc(who);
+      if (held + n > kRoom) {
+        __syncwarp();
+        const Key x = lane < held ? mine[lane] : 0, y = lane + 32 < held ? mine[lane + 32] : 0;
+        int rx = 0, ry = 0;
+        for (int i = 0; i < held; ++i) {
+          const Key q = mine[i];
+          rx += q > x;
+          ry += q > y;
+        }
+        __syncwarp();
+        if (lane < held && rx < k) mine[rx] = x;
+        if (lane + 32 < held && ry < k) mine[ry] = y;
+        __syncwarp();
+        held = k;  // more than 32 keys were held
+        set_limit(mine[k - 1] + 1);
+        if (lane == 0) atomicMax(&sh.hint, (uint32_t)(limit >> 32));
+      }
+      if (pass) mine[held + __popc(who & ((1u << lane) - 1))] = key;
+      held += n;
+    };
+
+    // the partial vectors: at the row's start this side of alignment, and behind its last whole one
+    if (part == 0 && warp == 0) {
+      const int tail = max((p.vocab + r.skew) / VEC, r.skew ? 1 : 0) * VEC - r.skew;
+      const int i = lane < VEC ? lane : tail + lane - VEC;
+      const bool in = lane < VEC ? r.skew && i < VEC - r.skew && i < p.vocab : lane < 2 * VEC && i < p.vocab;
+      const float f = in ? Vec<T>::one(r.x[i]) : -INFINITY;
+      most = fmaxf(f, -INFINITY);
+      if (most > -INFINITY) acc.lift(most, lifted);
+      acc.z = f == -INFINITY ? 0.f : (fabsf(f) < INFINITY ? ex2(acc.res) : NAN);
+      acc.s = acc.z * acc.res;
+      if (k > 0) push(f > -INFINITY ? make_key(f, i) : 0);
+    }
+
+    int chunk = 0, next_raise = 0;
+    for (int v0 = r.v0; v0 < r.v1; v0 += CH, ++chunk) {
+      mbar_wait(smem_addr(&sh.full[slot]), phase, dead);
+      const T* here = reinterpret_cast<const T*>(sh.ring[slot]);
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        raw[u] = reinterpret_cast<const uint4*>(here)[u * NT + tid];
+      }
+      if (v0 + CH > r.v1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * NT + tid >= r.v1) raw[u] = Vec<T>::none();
+      }
+      const float top = Vec<T>::top(raw);
+      most = fmaxf(most, top);
+      if (top > lifted) acc.lift(top, lifted);
+      F2 z2 = pack(0.f, 0.f), s2 = z2;
+      const F2 back = pack(-acc.c, -acc.c), scale = pack(kLog2e, kLog2e);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[VEC];
+        Vec<T>::get(raw[u], f);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          const F2 d = fma2(pack(f[i], f[i + 1]), scale, back);
+          float d0, d1;
+          unpack(d, d0, d1);
+          const F2 e = pack(ex2(d0), ex2(d1));
+          z2 = add2(z2, e);
+          s2 = fma2(e, d, s2);
+        }
+      }
+      float z0, z1, s0, s1;
+      unpack(z2, z0, z1);
+      unpack(s2, s0, s1);
+      float z = z0 + z1, s = s0 + s1;
+      if (!(s == s) || acc.huge) {
+        // 0 * -infinity (masked logits), a real NaN, or a reference too large for the fma:
+        // again, with the exponent bounded where 2^d is 0
+        z = s = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[VEC];
+          Vec<T>::get(raw[u], f);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float d = max_nan(acc.huge ? (f[i] - acc.m) * kLog2e : fmaf(f[i], kLog2e, -acc.c), -150.f), e = ex2(d);
+            z += e;
+            s = fmaf(e, d, s);
+          }
+        }
+      }
+      acc.z += z;
+      acc.s += s;
+
       if (k > 0) {
-        const int m = select_best<NT>(sh, n, k);
-        if (tid == 0) sh.n_best = m;
+        if (chunk == next_raise && (chunk == 0 || v0 + CH < r.v1)) {
+          // After chunks 1, 2, 4, ... (but not the last): raise the limit to the k-th
+          // largest maximum of the thread groups so far, which k keys reach; a
+          // group's threads share the comparisons of its maximum with the others.
+          next_raise = 2 * chunk + 1;
+          constexpr int GT = NT / kGroups;
+          uint32_t g = most > -INFINITY ? ordered(most) & ~(kGroups - 1u) : 0u;
+#pragma unroll
+          for (int o = GT / 2; o; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+          g |= tid / GT;  // no two are equal; a limit that is too low by less than kGroups steps is still one
+          if (tid % GT == 0) sh.tops[tid / GT] = g;
+          compute_bar<NT>();
+          int rank = 0;
+#pragma unroll
+          for (int i = 0; i < kGroups / GT; i += 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sh.tops + tid % GT * (kGroups / GT) + i);
+            rank += (w.x > g) + (w.y > g) + (w.z > g) + (w.w > g);
+          }
+#pragma unroll
+          for (int o = GT / 2; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+          if (rank == k - 1 && tid % GT == 0) sh.raised = g & ~(kGroups - 1u);
+          compute_bar<NT>();
+          set_limit((Key)max(sh.raised, *(volatile uint32_t*)&sh.hint) << 32);
+        }
+        // the warp looks through its candidates one by one, a lane a logit
+        uint32_t todo = __ballot_sync(0xffffffffu, top >= least);
+        while (todo) {
+          const int t = (tid & ~31) + __ffs(todo) - 1, u = lane / VEC, i = lane % VEC, v = v0 + u * NT + t;
+          todo &= todo - 1;
+          Key key = 0;
+          if (u < U && v < r.v1) {
+            const float f = Vec<T>::one(here[(u * NT + t) * VEC + i]);
+            if (f > -INFINITY) key = make_key(f, v * VEC - r.skew + i);
+          }
+          push(key);
+        }
       }
-      __syncthreads();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+      if (++slot == kStagesS) slot = 0, phase ^= 1;
     }
-    cluster.sync();  // a block's shared memory stays until it has been read
-    if (part) return;
-  }
-  const Sum r = sh.sum;
-  const float lnz = logf(r.z);
-  const bool none = !(r.z > 0.f) || isinf(r.m);  // NaN, infinities, or nothing allowed
-  if (tid == 0) {
-    const int t = p.tokens[row];
-    float v = NAN;
-    if (t >= 0 && t < p.vocab && !none) {
-      const float xt = sizeof(T) == 4 ? reinterpret_cast<const float*>(x)[t]
-                                      : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(x)[t] << 16);
-      v = xt - r.m - lnz;
+
+    // join the warps' sums and keys
+    Sum a = warp_join(acc.sum());
+    if (lane == 0) {
+      sh.part[warp] = a;
+      sh.held[warp] = held;
     }
-    p.logprob[row] = v;
-    if (p.entropy) p.entropy[row] = none ? NAN : lnz - kLn2 * r.s / r.z;
-  }
-  if (tid < k) {
-    const bool has = !none && tid < sh.n_best;
-    const Key key = has ? sh.best[tid] : 0;
-    p.ids[row * k + tid] = has ? (int32_t)~(uint32_t)key : -1;
-    p.tops[row * k + tid] = none ? NAN : (has ? from_ordered((uint32_t)(key >> 32)) - r.m - lnz : -INFINITY);
+    const Key ka = lane < held ? mine[lane] : 0, kb = lane + 32 < held ? mine[lane + 32] : 0;
+    compute_bar<NT>();
+    int n = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < S::kWarps; ++w) {
+      if (w == warp) before = n;
+      n += sh.held[w];
+    }
+    if (lane < held) sh.keys[before + lane] = ka;
+    if (lane + 32 < held) sh.keys[before + lane + 32] = kb;
+    if (warp == 0) {
+      a = warp_join(lane < S::kWarps ? sh.part[lane] : Sum{-INFINITY, 0.f, 0.f});
+      if (lane == 0) sh.sum = a;
+    }
+    compute_bar<NT>();
+    int got = min(n, k);
+    rank_keys(sh.keys, n, k, sh.best, tid, NT);
+    if (tid == 0) sh.n_best = got;
+    compute_bar<NT>();
+
+    if (parts > 1) {  // one row a cluster
+      cluster.sync();
+      if (part == 0) {
+        if (warp == 0) {
+          a = warp_join(lane < parts ? cluster.map_shared_rank(&sh, lane)->sum : Sum{-INFINITY, 0.f, 0.f});
+          if (lane == 0) sh.sum = a;
+        }
+        // the blocks' best keys side by side
+        n = 0;
+        for (int i = 0; i < parts; ++i) {
+          const S* o = cluster.map_shared_rank(&sh, i);
+          const int m = o->n_best;
+          if (tid < m) sh.keys[n + tid] = o->best[tid];
+          n += m;
+        }
+        compute_bar<NT>();
+        got = min(n, k);
+        rank_keys(sh.keys, n, k, sh.best, tid, NT);
+        compute_bar<NT>();
+      }
+      cluster.sync();  // a block's shared memory stays until it has been read
+    }
+    if (part == 0) {
+      const Sum q = sh.sum;
+      const float lnz = logf(q.z);
+      const bool none = !(q.z > 0.f) || isinf(q.m) || *dead;  // NaN, infinities, nothing allowed (or a copy that never came)
+      if (tid == 0) {
+        p.logprob[row] = none ? NAN : given - q.m - lnz;
+        if (p.entropy) p.entropy[row] = none ? NAN : lnz - kLn2 * q.s / q.z;
+      }
+      if (tid < k) {
+        const bool has = !none && tid < got;
+        const Key key = has ? sh.best[tid] : 0;
+        p.ids[(int64_t)row * k + tid] = has ? (int32_t)~(uint32_t)key : -1;
+        p.tops[(int64_t)row * k + tid] = none ? NAN : (has ? from_ordered((uint32_t)(key >> 32)) - q.m - lnz : -INFINITY);
+      }
+    }
+    compute_bar<NT>();  // the shared sums and keys are free for the next row
   }
 }
 
 template <typename T, int NT>
-cudaError_t launch(const ScoreParams& p, int rows, int parts, cudaStream_t stream) {
+cudaError_t launch(const ScoreParams& p, int parts, int n_sm, cudaStream_t stream) {
+  // per device and process, not per call: the limit is an attribute of the function
+  static std::atomic<uint64_t> prepared;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(prepared.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(score_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<NT>));
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  const int resident = parts > 1 ? p.rows : n_sm * (NT == 256 ? 3 : 6);  // rows at once
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * parts);
-  cfg.blockDim = dim3(NT);
+  cfg.gridDim = dim3((unsigned)std::min(p.rows, resident) * parts);
+  cfg.blockDim = dim3(NT + 32);
+  cfg.dynamicSmemBytes = sizeof(Shared<NT>);
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -322,12 +555,12 @@ cudaError_t launch(const ScoreParams& p, int rows, int parts, cudaStream_t strea
 }
 
 template <typename T>
-cudaError_t score(const ScoreParams& p, int rows, int n_sm, cudaStream_t stream) {
-  if (p.vocab <= 4096) return launch<T, 128>(p, rows, 1, stream);
+cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
+  if (p.vocab <= 4096) return launch<T, 128>(p, 1, n_sm, stream);
   // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least.
   int parts = 1;
-  while (parts < 8 && rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
-  return launch<T, 512>(p, rows, parts, stream);
+  while (parts < 8 && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
+  return launch<T, 256>(p, parts, n_sm, stream);
 }
 
 __global__ void advance_lens(int32_t* lens, int n) {
@@ -353,9 +586,9 @@ extern "C" int mk_token_logprobs(const void* logits, int dtype, int64_t row_stri
   mk::OnDevice here(device);
   const int n_sm = here.ok ? mk::current_sms() : 0;
   if (!n_sm) return MK_ERR_CUDA;
-  const mk::ScoreParams p{logits, row_stride, tokens, out_logprob, out_entropy, out_top_ids, out_top_logprobs, vocab, top_k};
-  const cudaError_t e = es == 2 ? mk::score<uint16_t>(p, n_rows, n_sm, (cudaStream_t)stream)
-                                : mk::score<float>(p, n_rows, n_sm, (cudaStream_t)stream);
+  const mk::ScoreParams p{logits, row_stride, tokens, out_logprob, out_entropy, out_top_ids, out_top_logprobs, vocab, top_k, n_rows};
+  const cudaError_t e = es == 2 ? mk::score<uint16_t>(p, n_sm, (cudaStream_t)stream)
+                                : mk::score<float>(p, n_sm, (cudaStream_t)stream);
   if (e == cudaSuccess) return MK_OK;
   cudaGetLastError();
   return MK_ERR_CUDA;
