@@ -5,16 +5,18 @@
 // KV head, the prefix serves batch x group rows at once (group = query heads
 // per KV head), a sequence's own positions serve its group rows.  Both are cut
 // into tiles of kTile positions; a "group" is the tiles of one set of rows
-// (prefix: KV head x row tile; own: sequence x KV head).  The tiles of all groups, in
-// order, are dealt to the blocks as equal contiguous runs; a block's run within
-// a group is a piece, which keeps the running maximum m and sum l of every row
-// (softmax in one pass) and its unnormalised output o, and leaves them in the
-// workspace.  A second kernel joins the pieces of a row:
+// (prefix: KV head x row tile; own: sequence x KV head).  The tiles of all
+// groups, in order, are dealt to the blocks as equal contiguous runs (a group
+// counts kHead tiles more: what starting and ending it costs); a block's run
+// within a group is a piece, which keeps the running maximum m and sum l of
+// every row (softmax in one pass) and its unnormalised output o, and leaves
+// them in the workspace.  A second kernel joins the pieces of a row:
 //   M = max m,  o = sum 2^(m - M) o / sum 2^(m - M) l,  lse = ln 2 (M + log2 sum 2^(m - M) l)
 // with scores in units of log2 (scale * log2 e folded into one factor).
 //
 // Bound: memory, 4 head_dim bytes of cache a position and KV head against
-// 4 head_dim flops a row; a producer warp keeps a ring of TMA boxes in flight.
+// 4 head_dim flops a row.  A producer warp keeps a ring of TMA boxes in flight;
+// two small blocks an SM, so that one streams while the other starts or ends a piece.
 #include <algorithm>
 
 #include "mk_cache.h"
@@ -25,34 +27,42 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 8;                        // compute warps; warp 8 is the producer
-constexpr int kAttThreads = kWarps * 32 + 32;
+constexpr int kTile = 64;                        // cache positions a tile
+constexpr int kWarps = 4;                        // compute warps; the next one is the producer
+constexpr int kComputeThreads = kWarps * 32;
+constexpr int kAttThreads = kComputeThreads + 32;
+constexpr int kBlocksPerSm = 2;
+constexpr int kHead = 2;                         // tiles that a group's start and end count as
 constexpr int kMaxRows = 64;                     // rows of a prefix row tile
 constexpr int kRedPitch = 64 + 4;                // floats a row of the joining buffer (64 columns at a time)
 
 template <int HD>
 struct Layout {
-  static constexpr int kSlotBytes = kTile * HD * 2;         // one tile of K or of V: [HD/64][128 rows][128 B], swizzled
-  static constexpr int kSlots = 160 * 1024 / kSlotBytes;
+  static constexpr int kSlotBytes = kTile * HD * 2;         // one tile of K or of V: [HD/64][kTile rows][128 B], swizzled
+  static constexpr int kSlots = 64 * 1024 / kSlotBytes;
   static constexpr int kRed = kSlots * kSlotBytes;          // float[kWarps][16][kRedPitch]
-  static constexpr int kMl = kRed + kWarps * 16 * kRedPitch * 4;  // float2[kWarps][16]
-  static constexpr int kCum = kMl + kWarps * 16 * 8;        // int[kCacheMaxBatch + 1]: own tiles of the sequences before
-  static constexpr int kLen = kCum + (kCacheMaxBatch + 4) * 4;    // int[kCacheMaxBatch]
-  static constexpr int kCtl = kLen + kCacheMaxBatch * 4;
-  static constexpr int kTotal = kCtl + 512 + 1024;          // 1024: the ring is aligned by hand
+  static constexpr int kQPitch = HD * 2 + 16;               // bytes a query row: ldmatrix rows in different banks
+  static constexpr int kQ = kRed + kWarps * 16 * kRedPitch * 4;  // two buffers of 32 rows, or one of 64
+  static constexpr int kMl = kQ + kMaxRows * kQPitch;       // float2[kWarps][16]
+  static constexpr int kCum = kMl + kWarps * 16 * 8;        // int[kCacheMaxBatch + 1]: cost of the sequences before
+  static constexpr int kCtl = kCum + (kCacheMaxBatch + 4) * 4;
+  static constexpr int kTotal = kCtl + 256 + 1024;          // 1024: the ring is aligned by hand
+  static_assert(kTotal <= 113 * 1024, "two blocks an SM");
 };
 
 struct Ctl {
-  unsigned long long full[20], empty[20];
+  unsigned long long full[8], empty[8], qfull[2], qempty[2];
   int dead, max_len;
 };
-static_assert(sizeof(Ctl) <= 512, "control block");
+static_assert(sizeof(Ctl) <= 256, "control block");
 
 struct AttendParams {
   CacheView c;
   int layer, group, box;
-  int prefix, base;        // own tiles start at base: prefix rounded down to a whole box of a paged cache
+  int whole;               // a tile that starts at a multiple of kTile (contiguous: anywhere) is one TMA box
+  int prefix, base;        // own tiles start at base: prefix rounded down so that no box crosses a page
   int row_tile, row_tiles; // prefix rows per group, row tiles per KV head
+  int wide;                // some piece has more than 32 rows: one query buffer
   float scale;             // scale * log2 e
   const uint16_t* q;
   const int32_t* seq_lens;
@@ -61,18 +71,19 @@ struct AttendParams {
   // workspace
   float *pre_o, *own_o;    // [piece][row_tile | group][hd]
   float2 *pre_ml, *own_ml; // [piece][rows]
-  int* sched;              // [0] prefix tiles a group, [2, 3] tiles (int64), [4...] own tiles of the sequences before (batch + 1)
+  int* sched;              // [0] prefix tiles a group, [2, 3] cost of all groups (int64), [4...] of the sequences before (batch + 1)
 };
 
-// Blocks that work: a block has at least one tile.
-__device__ __forceinline__ int active_blocks(int64_t tiles, int grid) { return (int)min(tiles, (int64_t)grid); }
-// First tile of block i of G, and the block that holds tile u.
-__device__ __forceinline__ int64_t first_tile(int64_t tiles, int i, int G) { return tiles * i / G; }
-__device__ __forceinline__ int block_of(int64_t u, int64_t tiles, int G) { return (int)(((u + 1) * G - 1) / tiles); }
+// Blocks that work, the first unit of cost of block i of G, and the block that holds unit u.
+__device__ __forceinline__ int active_blocks(int64_t cost, int grid) { return (int)min(cost, (int64_t)grid); }
+__device__ __forceinline__ int64_t first_unit(int64_t cost, int i, int G) { return cost * i / G; }
+__device__ __forceinline__ int block_of(int64_t u, int64_t cost, int G) { return (int)(((u + 1) * G - 1) / cost); }
 
 __device__ __forceinline__ int own_tiles(const AttendParams& p, int len) {
   return len > p.prefix ? (len - p.base + kTile - 1) / kTile : 0;
 }
+
+__device__ __forceinline__ void compute_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory"); }
 
 // A piece: tiles [i0, i1) of a group.
 struct Piece {
@@ -89,44 +100,54 @@ struct Walk {
   __device__ Walk(const AttendParams& prm, const int* cumulative, int pre, int64_t u0, int64_t u1)
       : p(prm), cum(cumulative), pre_tiles(pre), pre_groups(pre ? prm.c.nkv * prm.row_tiles : 0), u(u0), end(u1) {}
   __device__ __forceinline__ bool next(Piece& a) {
-    if (u >= end) return false;
-    const int64_t shared_tiles = (int64_t)pre_groups * pre_tiles;
-    int n;
-    if (u < shared_tiles) {
-      a.shared = true;
-      a.gidx = (int)(u / pre_tiles);
-      a.i0 = (int)(u % pre_tiles);
-      a.kvh = a.gidx / p.row_tiles;
-      a.tile0 = a.gidx % p.row_tiles * p.row_tile;
-      a.b = 0;
-      n = pre_tiles;
-    } else {
-      const int64_t v = u - shared_tiles;
-      const int w = (int)(v / p.c.nkv);
-      int lo = 0, hi = p.c.B;  // the sequence with cum[b] <= w < cum[b + 1]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (cum[mid] <= w) lo = mid; else hi = mid;
+    while (u < end) {
+      const int pre_cost = pre_tiles + kHead;
+      const int64_t shared_cost = (int64_t)pre_groups * pre_cost;
+      int n, r;  // cost of the group, place in it
+      if (u < shared_cost) {
+        a.shared = true;
+        a.gidx = (int)(u / pre_cost);
+        r = (int)(u % pre_cost);
+        a.kvh = a.gidx / p.row_tiles;
+        a.tile0 = a.gidx % p.row_tiles * p.row_tile;
+        a.b = 0;
+        n = pre_cost;
+      } else {
+        const int64_t v = u - shared_cost;
+        const int w = (int)(v / p.c.nkv);
+        int lo = 0, hi = p.c.B;  // the sequence with cum[b] <= w < cum[b + 1]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (cum[mid] <= w) lo = mid; else hi = mid;
+        }
+        n = cum[lo + 1] - cum[lo];
+        const int at = (int)(v - (int64_t)cum[lo] * p.c.nkv);
+        a.shared = false;
+        a.b = lo;
+        a.kvh = at / n;
+        r = at % n;
+        a.tile0 = 0;
+        a.gidx = lo * p.c.nkv + a.kvh;
       }
-      n = cum[lo + 1] - cum[lo];
-      const int r = (int)(v - (int64_t)cum[lo] * p.c.nkv);
-      a.shared = false;
-      a.b = lo;
-      a.kvh = r / n;
-      a.i0 = r % n;
-      a.tile0 = 0;
-      a.gidx = lo * p.c.nkv + a.kvh;
+      const int take = (int)min((int64_t)(n - r), end - u);
+      u += take;
+      a.i0 = max(r - kHead, 0);
+      a.i1 = r + take - kHead;
+      if (a.i1 > a.i0) return true;
     }
-    a.i1 = (int)min((int64_t)n, a.i0 + (end - u));
-    u += a.i1 - a.i0;
-    return true;
+    return false;
   }
 };
 
+__device__ __forceinline__ int piece_rows(const AttendParams& p, const Piece& a) {
+  return a.shared ? min(p.row_tile, p.c.B * p.group - a.tile0) : p.group;
+}
+
 template <int HD>
-__global__ void __launch_bounds__(kAttThreads, 1)
+__global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
     attend_tiles(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
-                 const __grid_constant__ CUtensorMap vmap) {
+                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kwhole,
+                 const __grid_constant__ CUtensorMap vwhole) {
   using S = Layout<HD>;
   constexpr int KS = HD / 16;  // k-steps of the score product
   constexpr int NT = HD / 8;   // column tiles of the output
@@ -136,7 +157,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   float* red = reinterpret_cast<float*>(smem + S::kRed);
   float2* sml = reinterpret_cast<float2*>(smem + S::kMl);
   int* cum = reinterpret_cast<int*>(smem + S::kCum);
-  int* lens = reinterpret_cast<int*>(smem + S::kLen);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + S::kCtl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const CacheView& c = p.c;
@@ -147,95 +167,140 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(smem_addr(&ctl->full[s]), 1);
       mbar_init(smem_addr(&ctl->empty[s]), kWarps);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&ctl->qfull[s]), 1);
+      mbar_init(smem_addr(&ctl->qempty[s]), kWarps);
+    }
     ctl->dead = 0;
     ctl->max_len = 0;
     fence_mbar_init();
   }
+  grid_launch_next();
+  // Lengths, and the cost of the sequences before each: a warp takes 32 at a
+  // time; with more, they are scanned once all have been read.
+  auto length = [&](int b) {
+    const int n = __ldg(p.seq_lens + b);
+    return n < 0 ? 0 : min(n, c.T);
+  };
   __syncthreads();
-  // lengths, and the tiles of the sequences before each
   int longest = 0;
   for (int b = tid; b < c.B; b += kAttThreads) {
-    int n = __ldg(p.seq_lens + b);
-    if (n < 0 || n > c.T) {
-      if (blockIdx.x == 0) set_status(c.status, MK_ERR_RANGE, b);
-      n = n < 0 ? 0 : c.T;
-    }
-    lens[b] = n;
-    longest = max(longest, n);
+    const int n = __ldg(p.seq_lens + b), m = n < 0 ? 0 : min(n, c.T);
+    if (n != m && blockIdx.x == 0) set_status(c.status, MK_ERR_RANGE, b);
+    const int t = own_tiles(p, m);
+    cum[b + 1] = t ? t + kHead : 0;
+    longest = max(longest, m);
   }
-  if (longest) atomicMax(&ctl->max_len, longest);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) atomicMax(&ctl->max_len, longest);
   __syncthreads();
   if (warp == 0) {
     int sum = 0;
     for (int b0 = 0; b0 < c.B; b0 += 32) {
       const int b = b0 + lane;
-      const int n = b < c.B ? own_tiles(p, lens[b]) : 0;
-      int x = n;
+      int x = b < c.B ? cum[b + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (b < c.B) cum[b] = sum + x - n;
+      if (b < c.B) cum[b + 1] = sum + x;
       sum += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) cum[c.B] = sum;
+    if (lane == 0) cum[0] = 0;
   }
   __syncthreads();
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int pre_tiles = (prefix_end + kTile - 1) / kTile;
-  const int64_t tiles = (int64_t)pre_tiles * p.row_tiles * c.nkv + (int64_t)cum[c.B] * c.nkv;
+  const int64_t cost = (pre_tiles ? (int64_t)(pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + (int64_t)cum[c.B] * c.nkv;
   if (blockIdx.x == 0) {
     for (int b = tid; b <= c.B; b += kAttThreads) p.sched[4 + b] = cum[b];
     if (tid == 0) {
       p.sched[0] = pre_tiles;
-      *reinterpret_cast<int64_t*>(p.sched + 2) = tiles;
+      *reinterpret_cast<int64_t*>(p.sched + 2) = cost;
     }
   }
-  const int G = active_blocks(tiles, gridDim.x), cta = blockIdx.x;
+  const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
   if (cta >= G) return;
-  Walk walk(p, cum, pre_tiles, first_tile(tiles, cta, G), first_tile(tiles, cta + 1, G));
+  Walk walk(p, cum, pre_tiles, first_unit(cost, cta, G), first_unit(cost, cta + 1, G));
   Piece a;
 
-  if (warp == kWarps) {  // ---- producer: K tile, V tile, K tile, ... into the ring
-    uint32_t slot = 0, phase = 0;
-    const int boxes = kTile / p.box;               // boxes of one 64-column block
+  if (warp == kWarps) {  // ---- producer: the pieces' query rows; K tile, V tile, K tile, ... into the ring
+    uint32_t slot = 0, phase = 0, qbuf = 0, qphase = 0;
+    const int boxes = kTile / p.box;               // boxes of one 64-column block of a tile that is no single box
     const int cb = lane / boxes, j = lane % boxes; // this lane's box
-    const bool mine = cb < HD / 64;
-    while (walk.next(a)) {
-      const int start = a.shared ? 0 : p.base, lo = a.shared ? 0 : p.prefix, hi = a.shared ? prefix_end : lens[a.b];
-      for (int i = a.i0; i < a.i1; ++i) {
-        const int t0 = start + i * kTile, at = t0 + j * p.box;
-        const bool wanted = mine && at < hi && at + p.box > lo;
-        bool ok = true;
-        int row = 0;
-        if (wanted) row = (int)(c.row(p.layer, a.b, at, &ok) + a.kvh * c.head_pitch());
-        if (!ok) set_status(c.status, MK_ERR_RANGE, a.b);
-        const int n = __popc(__ballot_sync(0xffffffffu, wanted));
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t full = smem_addr(&ctl->full[slot]);
-          mbar_wait(smem_addr(&ctl->empty[slot]), phase ^ 1, dead);
-          if (!__any_sync(0xffffffffu, *dead)) {
-            if (lane == 0) mbar_expect_tx(full, n * p.box * 128);
-            __syncwarp();
-            if (wanted)
-              tma_box2(ring + slot * S::kSlotBytes + cb * (kTile * 128) + j * p.box * 128, kv ? (const void*)&vmap : (const void*)&kmap,
-                       cb * 64, row, full);
-          }
-          __syncwarp();
-          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+    const bool boxed = cb < HD / 64;
+    int lo = 0, hi = 0, start = 0, i = 0, row = 0;
+    bool one = false, wanted = false;
+    // This lane's box of tile i of the piece.
+    auto place = [&]() {
+      const int t0 = start + i * kTile;
+      one = p.whole && t0 >= lo && t0 + kTile <= hi;
+      const int at = one ? t0 : t0 + j * p.box;
+      wanted = one ? lane == 0 : boxed && at < hi && at + p.box > lo;
+      bool ok = true;
+      if (wanted) row = (int)(c.row(p.layer, a.b, at, &ok) + a.kvh * c.head_pitch());
+      if (!ok) set_status(c.status, MK_ERR_RANGE, a.b);
+    };
+    auto open = [&]() {  // the next piece
+      if (!walk.next(a)) return false;
+      start = a.shared ? 0 : p.base;
+      lo = a.shared ? 0 : p.prefix;
+      hi = a.shared ? prefix_end : length(a.b);
+      i = a.i0;
+      place();
+      // its query rows
+      const int rows = piece_rows(p, a);
+      const uint32_t full = smem_addr(&ctl->qfull[qbuf]), dst = ring + S::kQ + qbuf * 32 * S::kQPitch;
+      mbar_wait(smem_addr(&ctl->qempty[qbuf]), qphase ^ 1, dead);
+      if (!__any_sync(0xffffffffu, *dead)) {
+        if (lane == 0) mbar_expect_tx(full, rows * HD * 2);
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32) {
+          const int b = a.shared ? (a.tile0 + r) / p.group : a.b, jh = a.shared ? (a.tile0 + r) % p.group : r;
+          bulk_load(dst + r * S::kQPitch, p.q + ((int64_t)b * c.nq + a.kvh * p.group + jh) * HD, HD * 2, full);
         }
       }
+      if (p.wide || qbuf) qphase ^= 1;
+      qbuf = p.wide ? 0 : qbuf ^ 1;
+      return true;
+    };
+    bool more = open();
+    while (more) {
+      const bool one_now = one, wanted_now = wanted;
+      const int row_now = row;
+      const uint32_t n = __popc(__ballot_sync(0xffffffffu, wanted_now));
+      const uint32_t bytes = one_now ? S::kSlotBytes : n * p.box * 128;
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t full = smem_addr(&ctl->full[slot]), dst = ring + slot * S::kSlotBytes;
+        mbar_wait(smem_addr(&ctl->empty[slot]), phase ^ 1, dead);
+        if (!__any_sync(0xffffffffu, *dead)) {
+          if (lane == 0) mbar_expect_tx(full, bytes);
+          __syncwarp();
+          if (wanted_now) {
+            if (one_now) tma_box3(dst, kv ? &vwhole : &kwhole, 0, row_now, 0, full);
+            else tma_box2(dst + cb * (kTile * 128) + j * p.box * 128, kv ? &vmap : &kmap, cb * 64, row_now, full);
+          }
+        }
+        __syncwarp();
+        if (++slot == S::kSlots) slot = 0, phase ^= 1;
+        if (kv == 0) {  // the next tile's place is looked up while this one's copies are under way
+          if (++i < a.i1) place();
+        }
+      }
+      if (i >= a.i1) more = open();
     }
     // a block that gave up waits for its own copies in flight before it ends
     if (__any_sync(0xffffffffu, *dead)) {
-      for (int s = 0; s < S::kSlots; ++s) {
-        const uint64_t t0 = globaltimer();
-        const uint32_t full = smem_addr(&ctl->full[s]);
-        // the slot's latest fill: the phase before the producer's next one
-        const uint32_t last = (uint32_t)s < slot ? phase : phase ^ 1;
-        while (!mbar_try(full, last) && globaltimer() - t0 < 10000000ull) {
+      const uint64_t t0 = globaltimer();
+      for (int s = 0; s < S::kSlots + 2; ++s) {
+        // the latest fill: the phase before the producer's next one
+        const bool ring_slot = s < S::kSlots;
+        const uint32_t full = smem_addr(ring_slot ? &ctl->full[s] : &ctl->qfull[s - S::kSlots]);
+        const uint32_t last = ring_slot ? ((uint32_t)s < slot ? phase : phase ^ 1)
+                                        : ((uint32_t)(s - S::kSlots) < qbuf ? qphase : qphase ^ 1);
+        while (!mbar_try(full, last) && globaltimer() - t0 < 20000000ull) {
         }
       }
       if (lane == 0) set_status(c.status, MK_ERR_DEVICE_TIMEOUT, cta);
@@ -244,30 +309,31 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 
   // ---- compute warps: rows as the mma's M (16 a row block), warps = row blocks x position splits
-  uint32_t slot = 0, phase = 0;
+  uint32_t slot = 0, phase = 0, qbuf = 0, qphase = 0;
   const int gq = lane / 4, cq = lane % 4;
   while (walk.next(a)) {
-    const int rows = a.shared ? min(p.row_tile, c.B * p.group - a.tile0) : p.group;
+    const int rows = piece_rows(p, a);
     const int R = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);  // row blocks
     const int rb = warp % R, sp = warp / R;
     const int lo = a.shared ? 0 : p.prefix, start = a.shared ? 0 : p.base;
-    const int hi = a.shared ? prefix_end : lens[a.b];
-    // this lane's two rows: their positions end at lim
-    int lim[2];
-    const uint16_t* qp[2];
+    const int hi = a.shared ? prefix_end : length(a.b);
+    int lim[2];  // positions of this lane's two rows end here
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = rb * 16 + gq + 8 * h;
-      const int b = a.shared ? (a.tile0 + r) / p.group : a.b, jh = a.shared ? (a.tile0 + r) % p.group : r;
-      lim[h] = r < rows ? min(lens[b], hi) : 0;
-      qp[h] = r < rows ? p.q + ((int64_t)b * c.nq + a.kvh * p.group + jh) * HD + cq * 2 : nullptr;
+      lim[h] = r >= rows ? 0 : (a.shared ? min(length((a.tile0 + r) / p.group), hi) : hi);
     }
     uint32_t qf[KS][4];
+    mbar_wait(smem_addr(&ctl->qfull[qbuf]), qphase, dead);
+    {
+      const uint32_t at = ring + S::kQ + (qbuf * 32 + rb * 16 + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        qf[k][e] = qp[e & 1] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e & 1] + k * 16 + (e >> 1) * 8)) : 0u;
+      for (int k = 0; k < KS; ++k) ldmatrix_x4(qf[k], at + k * 32);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&ctl->qempty[qbuf]));
+    if (p.wide || qbuf) qphase ^= 1;
+    qbuf = p.wide ? 0 : qbuf ^ 1;
 
     float o[NT][4];
 #pragma unroll
@@ -288,6 +354,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const int s0 = (sp * R + js) * 16, p0 = t0 + s0;
         if (p0 < hi && p0 + 16 > lo) {
           float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // odd k-steps: shorter chains
           {
             const int mi = lane >> 3, row = s0 + (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
@@ -295,8 +362,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
               const int ch = k * 2 + (mi & 1);
               uint32_t f[4];
               ldmatrix_x4(f, kslot + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-              mma16816(s[0], qf[k], f[0], f[1]);
-              mma16816(s[1], qf[k], f[2], f[3]);
+              mma16816(k & 1 ? u[0] : s[0], qf[k], f[0], f[1]);
+              mma16816(k & 1 ? u[1] : s[1], qf[k], f[2], f[3]);
             }
           }
           // mask, maximum
@@ -306,7 +373,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int pos = p0 + n * 8 + cq * 2 + (e & 1);
-              s[n][e] = pos >= lo && pos < lim[e >> 1] ? s[n][e] * p.scale : -INFINITY;
+              s[n][e] = pos >= lo && pos < lim[e >> 1] ? (s[n][e] + u[n][e]) * p.scale : -INFINITY;
               mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
             }
 #pragma unroll
@@ -380,40 +447,38 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (cq == 0) sml[warp * 16 + gq + 8 * h] = make_float2(m[h], l[h]);
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    float f[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float M = -INFINITY;
-      for (int w = rb; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + gq + 8 * h].x);
-      f[h] = M == -INFINITY ? 0.f : ex2(m[h] - M);
-    }
+    compute_bar();
     const int64_t pid = (int64_t)cta + a.gidx;
     const int stride = a.shared ? p.row_tile : p.group;
     float* po = (a.shared ? p.pre_o : p.own_o) + pid * stride * HD;
     float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * stride;
-    if (tid < rows) {
-      const int blk = tid / 16, r = tid % 16;
+    float f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = gq + 8 * h;
       float M = -INFINITY, L = 0.f;
-      for (int w = blk; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + r].x);
-      for (int w = blk; w < kWarps; w += R) {
-        const float2 x = sml[w * 16 + r];
-        if (x.y != 0.f) L += x.y * ex2(x.x - M);
+      for (int w = rb; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + r].x);
+      f[h] = M == -INFINITY ? 0.f : ex2(m[h] - M);
+      if (sp == 0 && cq == 0 && rb * 16 + r < rows) {
+        for (int w = rb; w < kWarps; w += R) {
+          const float2 x = sml[w * 16 + r];
+          if (x.y != 0.f) L += x.y * ex2(x.x - M);
+        }
+        pml[rb * 16 + r] = make_float2(M, L);
       }
-      pml[tid] = make_float2(M, L);
     }
 #pragma unroll
     for (int half = 0; half < HD / 64; ++half) {
-      if (half) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (half) compute_bar();
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const float* v = o[half * 8 + n];
         float* d = red + (warp * 16 + gq) * kRedPitch + n * 8 + cq * 2;
-        *reinterpret_cast<float2*>(d) = make_float2(v[0] * f[0], v[1] * f[0]);
-        *reinterpret_cast<float2*>(d + 8 * kRedPitch) = make_float2(v[2] * f[1], v[3] * f[1]);
+        if (rb * 16 + gq < rows) *reinterpret_cast<float2*>(d) = make_float2(v[0] * f[0], v[1] * f[0]);
+        if (rb * 16 + gq + 8 < rows) *reinterpret_cast<float2*>(d + 8 * kRedPitch) = make_float2(v[2] * f[1], v[3] * f[1]);
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      for (int e = tid; e < rows * 16; e += kWarps * 32) {
+      compute_bar();
+      for (int e = tid; e < rows * 16; e += kComputeThreads) {
         const int r = e / 16, col = e % 16 * 4;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = r / 16; w < kWarps; w += R) {
@@ -423,56 +488,78 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         *reinterpret_cast<float4*>(po + (int64_t)r * HD + half * 64 + col) = sum;
       }
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");  // sml and red are free for the next piece
+    compute_bar();  // sml and red are free for the next piece
   }
 }
 
-// Joins the pieces of every row: a warp a row, block (b) x row group.
+// Joins the pieces of every row: a warp a row.
 template <int HD>
-__global__ void __launch_bounds__(256) attend_join(const __grid_constant__ AttendParams p, int grid) {
+__global__ void __launch_bounds__(128) attend_join(const __grid_constant__ AttendParams p, int grid) {
   constexpr int V = HD / 32;
   const CacheView& c = p.c;
-  const int b = blockIdx.x, head = blockIdx.y * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (head >= c.nq) return;
+  const int64_t task = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int b = (int)(task / c.nq), head = (int)(task % c.nq), lane = threadIdx.x % 32;
+  grid_wait();
+  if (b >= c.B) return;
   const int kvh = head / p.group, j = head % p.group;
   const int pre_tiles = p.sched[0], cum0 = p.sched[4 + b], own = p.sched[5 + b] - cum0;
-  const int64_t tiles = *reinterpret_cast<const int64_t*>(p.sched + 2);
-  const int G = active_blocks(tiles, grid);
-  const int64_t shared_tiles = (int64_t)pre_tiles * p.row_tiles * c.nkv;
+  const int64_t cost = *reinterpret_cast<const int64_t*>(p.sched + 2);
+  const int G = active_blocks(cost, grid);
 
-  float M = -INFINITY, L = 0.f, o[V] = {};
-  auto take = [&](const float2* ml, const float* po) {
-    const float2 x = *ml;
-    if (x.y == 0.f) return;  // every position masked (a NaN sum is passed on)
-    const float m = fmaxf(M, x.x), fa = M == -INFINITY ? 0.f : ex2(M - m), fb = ex2(x.x - m);
-    L = L * fa + x.y * fb;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = o[i] * fa + po[lane * V + i] * fb;
-    M = m;
-  };
+  // the row's pieces: blocks [b0, b0 + n0) of the prefix, [b1, b1 + n1) of its own positions
+  int n0 = 0, n1 = 0;
+  int64_t at0 = 0, at1 = 0;
+  const int64_t pre_cost = pre_tiles ? pre_tiles + kHead : 0;
   if (pre_tiles) {
-    const int row = b * p.group + j, gidx = kvh * p.row_tiles + row / p.row_tile, r = row % p.row_tile;
-    const int64_t u0 = (int64_t)gidx * pre_tiles;
-    const int last = block_of(u0 + pre_tiles - 1, tiles, G);
-    for (int i = block_of(u0, tiles, G); i <= last; ++i) {
-      const int64_t at = (int64_t)(i + gidx) * p.row_tile + r;
-      take(p.pre_ml + at, p.pre_o + at * HD);
-    }
+    const int row = b * p.group + j, gidx = kvh * p.row_tiles + row / p.row_tile;
+    const int64_t u0 = gidx * pre_cost + kHead;
+    const int b0 = block_of(u0, cost, G);
+    n0 = block_of(u0 + pre_tiles - 1, cost, G) - b0 + 1;
+    at0 = (int64_t)(b0 + gidx) * p.row_tile + row % p.row_tile;
   }
   if (own) {
     const int gidx = b * c.nkv + kvh;
-    const int64_t u0 = shared_tiles + (int64_t)cum0 * c.nkv + (int64_t)kvh * own;
-    const int last = block_of(u0 + own - 1, tiles, G);
-    for (int i = block_of(u0, tiles, G); i <= last; ++i) {
-      const int64_t at = (int64_t)(i + gidx) * p.group + j;
-      take(p.own_ml + at, p.own_o + at * HD);
+    const int64_t u0 = pre_cost * p.row_tiles * c.nkv + (int64_t)cum0 * c.nkv + (int64_t)kvh * own + kHead;
+    const int b1 = block_of(u0, cost, G);
+    n1 = block_of(u0 + own - kHead - 1, cost, G) - b1 + 1;
+    at1 = (int64_t)(b1 + gidx) * p.group + j;
+  }
+  float M = -INFINITY, L = 0.f, o[V] = {};
+  for (int i0 = 0; i0 < n0 + n1; i0 += 32) {  // 32 pieces at a time: a lane's weight, then the weighted sum
+    const int i = i0 + lane;
+    const int64_t at = i < n0 ? at0 + (int64_t)i * p.row_tile : at1 + (int64_t)(i - n0) * p.group;
+    const float2 x = i < n0 ? p.pre_ml[at] : (i < n0 + n1 ? p.own_ml[at] : make_float2(-INFINITY, 0.f));
+    float m = x.x;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    m = fmaxf(m, M);
+    const float ref = m == -INFINITY ? 0.f : m, back = ex2(M - ref);
+    const float w = x.y == 0.f ? 0.f : ex2(x.x - ref);  // a piece without positions has no part (a NaN sum is passed on)
+    float l = w * x.y;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+    L = L * back + l;
+    M = m;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= back;
+    const int n = min(32, n0 + n1 - i0);
+#pragma unroll 4
+    for (int q = 0; q < n; ++q) {
+      const int iq = i0 + q;
+      const float* po = iq < n0 ? p.pre_o + (at0 + (int64_t)iq * p.row_tile) * HD : p.own_o + (at1 + (int64_t)(iq - n0) * p.group) * HD;
+      const float wq = __shfl_sync(0xffffffffu, w, q);
+      float v[V];
+      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po + lane * 4);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po + lane * 2);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = wq == 0.f ? o[e] : fmaf(v[e], wq, o[e]);
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;  // a row without positions: zeros
   const int64_t at = (int64_t)b * c.nq + head;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * HD + lane * V);
 #pragma unroll
-  for (int i = 0; i < V; i += 2) out[i / 2] = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+  for (int e = 0; e < V; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   if (p.lse && lane == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
 }
 
@@ -496,8 +583,9 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
   w.row_tile = std::min((rows + 15) / 16 * 16, kMaxRows);
   w.row_tiles = (rows + w.row_tile - 1) / w.row_tile;
   // a piece more than its predecessor starts a block or a group: at most blocks + groups of them
-  const size_t pre = ((size_t)n_sm + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
-  const size_t own = ((size_t)n_sm + (size_t)d.n_kv_heads * d.batch) * group;
+  const size_t blocks = (size_t)n_sm * kBlocksPerSm;
+  const size_t pre = (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
+  const size_t own = (blocks + (size_t)d.n_kv_heads * d.batch) * group;
   Carve cv;
   w.sched = cv.take(sizeof(int) * (d.batch + 5));
   w.pre_o = cv.take(pre * d.head_dim * sizeof(float));
@@ -509,12 +597,22 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
 }
 
 template <int HD>
-cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
-  attend_tiles<HD><<<c.n_sm, kAttThreads, Layout<HD>::kTotal, stream>>>(p, c.kmap, c.vmap);
+cudaError_t run(AttendParams p, const mk_cache& c, cudaStream_t stream) {
+  const int grid = c.n_sm * kBlocksPerSm;
+  attend_tiles<HD><<<grid, kAttThreads, Layout<HD>::kTotal, stream>>>(p, c.kmap, c.vmap, c.kwhole, c.vwhole);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attend_join<HD><<<dim3(c.d.batch, (c.d.n_q_heads + 7) / 8), 256, 0, stream>>>(p, c.n_sm);
-  return cudaGetLastError();
+  // the join's blocks are set up while the tiles are still under way
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)c.d.batch * c.d.n_q_heads + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join<HD>, p, grid);
 }
 
 }  // namespace
@@ -522,7 +620,7 @@ cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
 size_t attend_workspace(const mk_cache_desc& d, int n_sm) { return plan(d, n_sm).total; }
 
 cudaError_t attend_prepare() {
-  static_assert(Layout<64>::kSlots <= 20 && Layout<128>::kSlots <= 20, "barriers of the ring");
+  static_assert(Layout<64>::kSlots <= 8 && Layout<128>::kSlots <= 8, "barriers of the ring");
   cudaError_t e = cudaFuncSetAttribute(attend_tiles<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<64>::kTotal);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attend_tiles<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kTotal);
@@ -537,10 +635,12 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.layer = layer;
   p.group = c.d.n_q_heads / c.d.n_kv_heads;
   p.box = c.box;
+  p.whole = !c.view.bt || c.view.page % kTile == 0;
   p.prefix = prefix_len;
-  p.base = c.view.bt ? prefix_len / c.box * c.box : prefix_len;
+  p.base = !c.view.bt ? prefix_len : prefix_len / (p.whole ? kTile : c.box) * (p.whole ? kTile : c.box);
   p.row_tile = w.row_tile;
   p.row_tiles = w.row_tiles;
+  p.wide = std::max(p.group, prefix_len ? w.row_tile : 0) > 32;
   p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * 1.44269504088896341f;
   p.q = (const uint16_t*)q;
   p.seq_lens = seq_lens;

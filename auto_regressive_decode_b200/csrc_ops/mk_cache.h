@@ -14,7 +14,7 @@ namespace mk {
 constexpr int kCacheMaxBatch = 1024;  // sequences of a cache handle
 constexpr int kCacheMaxGroup = 64;    // query heads per KV head
 constexpr int kCachePageUnit = 16;    // page_size is a multiple of this
-constexpr int kTile = 128;            // cache positions per attention tile
+constexpr int kWholeRows = 64;        // cache rows of a whole box of the tensor maps: an attention tile
 
 // What a kernel needs to find a row of the cache: contiguous
 // [L][B][nkv][T][hd], or pages [L][n_pages][nkv][page][hd] through bt[B][bt_stride].
@@ -39,7 +39,7 @@ struct CacheView {
   __device__ __forceinline__ int64_t head_pitch() const { return bt ? page : T; }
 };
 
-// Rows of one TMA box of the cache maps: a box lies in one page.
+// Rows of a small TMA box of the cache: it lies in one page.
 inline int cache_box_rows(int page) {
   if (!page) return 32;
   int r = 32;
@@ -84,6 +84,7 @@ struct mk_cache {
   uint16_t *k, *v;
   int device, n_sm, box;
   float2* rope;  // [max_ctx][hd/2] (cos, sin)
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap;      // boxes of 64 columns x box rows
+  CUtensorMap kwhole, vwhole;  // boxes of all columns x kWholeRows rows
   void* region;
 };
