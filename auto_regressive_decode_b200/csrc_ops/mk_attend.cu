@@ -71,13 +71,13 @@ struct AttendParams {
   // workspace
   float *pre_o, *own_o;    // [piece][row_tile | group][hd]
   float2 *pre_ml, *own_ml; // [piece][rows]
-  int* sched;              // [0] prefix tiles a group, [2, 3] cost of all groups (int64), [4...] of the sequences before (batch + 1)
+  int2 *pre_blocks, *own_blocks;  // [group] first and last block with a piece of it
+  int* sched;              // [0] prefix tiles a group, [1...] own tiles of each sequence
 };
 
-// Blocks that work, the first unit of cost of block i of G, and the block that holds unit u.
+// Blocks that work, and the first unit of cost of block i of G.
 __device__ __forceinline__ int active_blocks(int64_t cost, int grid) { return (int)min(cost, (int64_t)grid); }
 __device__ __forceinline__ int64_t first_unit(int64_t cost, int i, int G) { return cost * i / G; }
-__device__ __forceinline__ int block_of(int64_t u, int64_t cost, int G) { return (int)(((u + 1) * G - 1) / cost); }
 
 __device__ __forceinline__ int own_tiles(const AttendParams& p, int len) {
   return len > p.prefix ? (len - p.base + kTile - 1) / kTile : 0;
@@ -90,6 +90,7 @@ struct Piece {
   bool shared;
   int b, kvh, tile0;  // own: the sequence; shared: first row of the row tile
   int i0, i1, gidx;
+  bool last;          // it ends its group
 };
 
 struct Walk {
@@ -133,6 +134,7 @@ struct Walk {
       u += take;
       a.i0 = max(r - kHead, 0);
       a.i1 = r + take - kHead;
+      a.last = r + take == n;
       if (a.i1 > a.i0) return true;
     }
     return false;
@@ -215,11 +217,8 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
   const int pre_tiles = (prefix_end + kTile - 1) / kTile;
   const int64_t cost = (pre_tiles ? (int64_t)(pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + (int64_t)cum[c.B] * c.nkv;
   if (blockIdx.x == 0) {
-    for (int b = tid; b <= c.B; b += kAttThreads) p.sched[4 + b] = cum[b];
-    if (tid == 0) {
-      p.sched[0] = pre_tiles;
-      *reinterpret_cast<int64_t*>(p.sched + 2) = cost;
-    }
+    for (int b = tid; b < c.B; b += kAttThreads) p.sched[1 + b] = cum[b + 1] - cum[b];
+    if (tid == 0) p.sched[0] = pre_tiles;
   }
   const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
   if (cta >= G) return;
@@ -449,6 +448,11 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
     }
     compute_bar();
     const int64_t pid = (int64_t)cta + a.gidx;
+    if (tid == 0) {
+      int2* at = (a.shared ? p.pre_blocks : p.own_blocks) + a.gidx;
+      if (a.i0 == 0) at->x = cta;
+      if (a.last) at->y = cta;
+    }
     const int stride = a.shared ? p.row_tile : p.group;
     float* po = (a.shared ? p.pre_o : p.own_o) + pid * stride * HD;
     float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * stride;
@@ -492,43 +496,34 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
   }
 }
 
-// Joins the pieces of every row: a warp a row.
-template <int HD>
-__global__ void __launch_bounds__(128) attend_join(const __grid_constant__ AttendParams p, int grid) {
+// Joins the pieces of every row: W warps a row take them in turn.
+template <int HD, int W>
+__global__ void __launch_bounds__(128) attend_join(const __grid_constant__ AttendParams p) {
   constexpr int V = HD / 32;
+  __shared__ float so[4][HD];
+  __shared__ float2 sml[4];
   const CacheView& c = p.c;
-  const int64_t task = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int b = (int)(task / c.nq), head = (int)(task % c.nq), lane = threadIdx.x % 32;
-  grid_wait();
-  if (b >= c.B) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % W;
+  const int64_t task = (int64_t)blockIdx.x * (4 / W) + warp / W;
+  const int b = (int)(task / c.nq), head = (int)(task % c.nq);
   const int kvh = head / p.group, j = head % p.group;
-  const int pre_tiles = p.sched[0], cum0 = p.sched[4 + b], own = p.sched[5 + b] - cum0;
-  const int64_t cost = *reinterpret_cast<const int64_t*>(p.sched + 2);
-  const int G = active_blocks(cost, grid);
+  const int row = b * p.group + j, g0 = kvh * p.row_tiles + row / p.row_tile, g1 = b * c.nkv + kvh;
+  grid_wait();
+  const bool have = b < c.B;
+  // the row's pieces: blocks [x, y] of its prefix group and of its own
+  int2 r0 = make_int2(0, -1), r1 = r0;
+  if (have && p.prefix) r0 = p.pre_blocks[g0];
+  if (have) r1 = p.own_blocks[g1];
+  if (p.prefix && p.sched[0] == 0) r0 = make_int2(0, -1);  // no sequence reaches into the prefix: its groups have no pieces
+  if (have && p.sched[1 + b] == 0) r1 = make_int2(0, -1);  // nor this sequence beyond it
+  const int n0 = r0.y - r0.x + 1, n = n0 + r1.y - r1.x + 1;
+  const int64_t at0 = (int64_t)(r0.x + g0) * p.row_tile + row % p.row_tile, at1 = (int64_t)(r1.x + g1) * p.group + j;
 
-  // the row's pieces: blocks [b0, b0 + n0) of the prefix, [b1, b1 + n1) of its own positions
-  int n0 = 0, n1 = 0;
-  int64_t at0 = 0, at1 = 0;
-  const int64_t pre_cost = pre_tiles ? pre_tiles + kHead : 0;
-  if (pre_tiles) {
-    const int row = b * p.group + j, gidx = kvh * p.row_tiles + row / p.row_tile;
-    const int64_t u0 = gidx * pre_cost + kHead;
-    const int b0 = block_of(u0, cost, G);
-    n0 = block_of(u0 + pre_tiles - 1, cost, G) - b0 + 1;
-    at0 = (int64_t)(b0 + gidx) * p.row_tile + row % p.row_tile;
-  }
-  if (own) {
-    const int gidx = b * c.nkv + kvh;
-    const int64_t u0 = pre_cost * p.row_tiles * c.nkv + (int64_t)cum0 * c.nkv + (int64_t)kvh * own + kHead;
-    const int b1 = block_of(u0, cost, G);
-    n1 = block_of(u0 + own - kHead - 1, cost, G) - b1 + 1;
-    at1 = (int64_t)(b1 + gidx) * p.group + j;
-  }
   float M = -INFINITY, L = 0.f, o[V] = {};
-  for (int i0 = 0; i0 < n0 + n1; i0 += 32) {  // 32 pieces at a time: a lane's weight, then the weighted sum
-    const int i = i0 + lane;
-    const int64_t at = i < n0 ? at0 + (int64_t)i * p.row_tile : at1 + (int64_t)(i - n0) * p.group;
-    const float2 x = i < n0 ? p.pre_ml[at] : (i < n0 + n1 ? p.own_ml[at] : make_float2(-INFINITY, 0.f));
+  for (int i0 = sub; i0 < n; i0 += 32 * W) {  // 32 pieces at a time: a lane's weight, then the weighted sum
+    const int i = i0 + lane * W;
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (i < n) x = i < n0 ? p.pre_ml[at0 + (int64_t)i * p.row_tile] : p.own_ml[at1 + (int64_t)(i - n0) * p.group];
     float m = x.x;
 #pragma unroll
     for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
@@ -542,19 +537,42 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
     M = m;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] *= back;
-    const int n = min(32, n0 + n1 - i0);
-#pragma unroll 4
-    for (int q = 0; q < n; ++q) {
-      const int iq = i0 + q;
+    const int k = min(32, (n - i0 + W - 1) / W);
+#pragma unroll 8
+    for (int q = 0; q < k; ++q) {
+      const int iq = i0 + q * W;
       const float* po = iq < n0 ? p.pre_o + (at0 + (int64_t)iq * p.row_tile) * HD : p.own_o + (at1 + (int64_t)(iq - n0) * p.group) * HD;
-      const float wq = __shfl_sync(0xffffffffu, w, q);
       float v[V];
       if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po + lane * 4);
       else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po + lane * 2);
+      const float wq = __shfl_sync(0xffffffffu, w, q);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = wq == 0.f ? o[e] : fmaf(v[e], wq, o[e]);
     }
   }
+  if (W > 1) {  // the warps' parts
+#pragma unroll
+    for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+    if (lane == 0) sml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (sub) return;
+    const float mine = M;
+#pragma unroll
+    for (int w = 1; w < W; ++w) M = fmaxf(M, sml[warp + w].x);
+    const float ref = M == -INFINITY ? 0.f : M, f = ex2(mine - ref);
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= f;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float2 x = sml[warp + w];
+      const float g = x.y == 0.f ? 0.f : ex2(x.x - ref);
+      L += g * x.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = g == 0.f ? o[e] : fmaf(so[warp + w][lane * V + e], g, o[e]);
+    }
+  }
+  if (!have) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;  // a row without positions: zeros
   const int64_t at = (int64_t)b * c.nq + head;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * HD + lane * V);
@@ -574,7 +592,7 @@ struct Carve {
 };
 struct Plan {
   int row_tile, row_tiles;
-  size_t sched, pre_o, pre_ml, own_o, own_ml, total;
+  size_t sched, pre_blocks, own_blocks, pre_o, pre_ml, own_o, own_ml, total;
 };
 
 Plan plan(const mk_cache_desc& d, int n_sm) {
@@ -587,7 +605,9 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
   const size_t pre = (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
   const size_t own = (blocks + (size_t)d.n_kv_heads * d.batch) * group;
   Carve cv;
-  w.sched = cv.take(sizeof(int) * (d.batch + 5));
+  w.sched = cv.take(sizeof(int) * (d.batch + 1));
+  w.pre_blocks = cv.take(sizeof(int2) * d.n_kv_heads * w.row_tiles);
+  w.own_blocks = cv.take(sizeof(int2) * d.n_kv_heads * d.batch);
   w.pre_o = cv.take(pre * d.head_dim * sizeof(float));
   w.pre_ml = cv.take(pre * sizeof(float2));
   w.own_o = cv.take(own * d.head_dim * sizeof(float));
@@ -603,8 +623,11 @@ cudaError_t run(AttendParams p, const mk_cache& c, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join's blocks are set up while the tiles are still under way
+  // Few rows: four warps each, since a row then has many pieces; else the SMs are busy with a warp a row.
+  const int64_t rows = (int64_t)c.d.batch * c.d.n_q_heads;
+  const bool few = rows <= 8 * c.n_sm;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)c.d.batch * c.d.n_q_heads + 3) / 4));
+  cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at;
@@ -612,7 +635,7 @@ cudaError_t run(AttendParams p, const mk_cache& c, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join<HD>, p, grid);
+  return few ? cudaLaunchKernelEx(&cfg, attend_join<HD, 4>, p) : cudaLaunchKernelEx(&cfg, attend_join<HD, 1>, p);
 }
 
 }  // namespace
@@ -647,6 +670,8 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.out = (uint16_t*)out;
   p.lse = lse;
   p.sched = (int*)(ws + w.sched);
+  p.pre_blocks = (int2*)(ws + w.pre_blocks);
+  p.own_blocks = (int2*)(ws + w.own_blocks);
   p.pre_o = (float*)(ws + w.pre_o);
   p.pre_ml = (float2*)(ws + w.pre_ml);
   p.own_o = (float*)(ws + w.own_o);
