@@ -12,8 +12,8 @@ SOURCES = ["mk_kernel.cu", "mk_api.cu", "mk_plan.cpp", "mk_noalloc.cu", "mk_tmap
 HEADERS = ["mk_internal.h", "mk_device.h"]
 # the operators around the decode step: cache append, attention over a shared prefix, token scores
 OPS = os.path.join(HERE, "csrc_ops")
-OPS_SOURCES = ["mk_cache.cu", "mk_append.cu", "mk_attend.cu", "mk_score.cu"]
-OPS_HEADERS = ["mk_cache.h", "mk_ptx.h"]
+OPS_SOURCES = ["mk_cache.cu", "mk_append.cu", "mk_attend.cu", "mk_attend_tc.cu", "mk_score.cu"]
+OPS_HEADERS = ["mk_attend.h", "mk_cache.h", "mk_ptx.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-Xcompiler", "-fPIC",
          "-shared", "-cudart", "static"]

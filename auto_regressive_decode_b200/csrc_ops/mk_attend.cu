@@ -19,7 +19,7 @@
 // two small blocks an SM, so that one streams while the other starts or ends a piece.
 #include <algorithm>
 
-#include "mk_cache.h"
+#include "mk_attend.h"
 #include "mk_ptx.h"
 
 namespace mk {
@@ -34,6 +34,7 @@ constexpr int kAttThreads = kComputeThreads + 32;
 constexpr int kBlocksPerSm = 2;
 constexpr int kHead = 2;                         // tiles that a group's start and end count as
 constexpr int kMaxRows = 64;                     // rows of a prefix row tile
+constexpr int kTcFrom = 16;                      // more rows of a KV head than this share a prefix: tensor-core kernel
 constexpr int kRedPitch = 64 + 4;                // floats a row of the joining buffer (64 columns at a time)
 
 template <int HD>
@@ -55,29 +56,6 @@ struct Ctl {
   int dead, max_len;
 };
 static_assert(sizeof(Ctl) <= 256, "control block");
-
-struct AttendParams {
-  CacheView c;
-  int layer, group, box;
-  int whole;               // a tile that starts at a multiple of kTile (contiguous: anywhere) is one TMA box
-  int prefix, base;        // own tiles start at base: prefix rounded down so that no box crosses a page
-  int row_tile, row_tiles; // prefix rows per group, row tiles per KV head
-  int wide;                // some piece has more than 32 rows: one query buffer
-  float scale;             // scale * log2 e
-  const uint16_t* q;
-  const int32_t* seq_lens;
-  uint16_t* out;
-  float* lse;
-  // workspace
-  float *pre_o, *own_o;    // [piece][row_tile | group][hd]
-  float2 *pre_ml, *own_ml; // [piece][rows]
-  int2 *pre_blocks, *own_blocks;  // [group] first and last block with a piece of it
-  int* sched;              // [0] prefix tiles a group, [1...] own tiles of each sequence
-};
-
-// Blocks that work, and the first unit of cost of block i of G.
-__device__ __forceinline__ int active_blocks(int64_t cost, int grid) { return (int)min(cost, (int64_t)grid); }
-__device__ __forceinline__ int64_t first_unit(int64_t cost, int i, int G) { return cost * i / G; }
 
 __device__ __forceinline__ int own_tiles(const AttendParams& p, int len) {
   return len > p.prefix ? (len - p.base + kTile - 1) / kTile : 0;
@@ -214,14 +192,17 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
   __syncthreads();
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
-  const int pre_tiles = (prefix_end + kTile - 1) / kTile;
+  const int pre_tiles = p.tc ? 0 : (prefix_end + kTile - 1) / kTile;
   const int64_t cost = (pre_tiles ? (int64_t)(pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + (int64_t)cum[c.B] * c.nkv;
   if (blockIdx.x == 0) {
     for (int b = tid; b < c.B; b += kAttThreads) p.sched[1 + b] = cum[b + 1] - cum[b];
-    if (tid == 0) p.sched[0] = pre_tiles;
+    if (tid == 0) p.sched[0] = prefix_end;
   }
   const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
-  if (cta >= G) return;
+  if (cta >= G) {
+    grid_wait();
+    return;
+  }
   Walk walk(p, cum, pre_tiles, first_unit(cost, cta, G), first_unit(cost, cta + 1, G));
   Piece a;
 
@@ -304,6 +285,7 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
       }
       if (lane == 0) set_status(c.status, MK_ERR_DEVICE_TIMEOUT, cta);
     }
+    grid_wait();
     return;
   }
 
@@ -494,6 +476,8 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
     }
     compute_bar();  // sml and red are free for the next piece
   }
+  // launched while attend_prefix_tc runs, this grid ends after it: the join waits for this one alone
+  grid_wait();
 }
 
 // Joins the pieces of every row: W warps a row take them in turn.
@@ -507,7 +491,12 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   const int64_t task = (int64_t)blockIdx.x * (4 / W) + warp / W;
   const int b = (int)(task / c.nq), head = (int)(task % c.nq);
   const int kvh = head / p.group, j = head % p.group;
-  const int row = b * p.group + j, g0 = kvh * p.row_tiles + row / p.row_tile, g1 = b * c.nkv + kvh;
+  const int row = b * p.group + j, g1 = b * c.nkv + kvh;
+  // the prefix's pieces are entries of some rows: one a piece, or of kTcRows rows, two a piece: for
+  // two row tiles, or, with one row tile in the group, for its even and odd tiles
+  const int entry = p.tc ? kTcRows : p.row_tile, per = p.tc ? 2 * kTcRows : entry;
+  const int g0 = p.tc ? kvh * p.tc_groups + row / per : kvh * p.row_tiles + row / per;
+  const bool both = p.tc && c.B * p.group - row / per * per <= kTcRows;
   grid_wait();
   const bool have = b < c.B;
   // the row's pieces: blocks [x, y] of its prefix group and of its own
@@ -516,14 +505,14 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   if (have) r1 = p.own_blocks[g1];
   if (p.prefix && p.sched[0] == 0) r0 = make_int2(0, -1);  // no sequence reaches into the prefix: its groups have no pieces
   if (have && p.sched[1 + b] == 0) r1 = make_int2(0, -1);  // nor this sequence beyond it
-  const int n0 = r0.y - r0.x + 1, n = n0 + r1.y - r1.x + 1;
-  const int64_t at0 = (int64_t)(r0.x + g0) * p.row_tile + row % p.row_tile, at1 = (int64_t)(r1.x + g1) * p.group + j;
+  const int n0 = (r0.y - r0.x + 1) * (both ? 2 : 1), n = n0 + r1.y - r1.x + 1, step = both ? entry : per;
+  const int64_t at0 = (int64_t)(r0.x + g0) * per + (both ? row % entry : row % per), at1 = (int64_t)(r1.x + g1) * p.group + j;
 
   float M = -INFINITY, L = 0.f, o[V] = {};
   for (int i0 = sub; i0 < n; i0 += 32 * W) {  // 32 pieces at a time: a lane's weight, then the weighted sum
     const int i = i0 + lane * W;
     float2 x = make_float2(-INFINITY, 0.f);
-    if (i < n) x = i < n0 ? p.pre_ml[at0 + (int64_t)i * p.row_tile] : p.own_ml[at1 + (int64_t)(i - n0) * p.group];
+    if (i < n) x = i < n0 ? p.pre_ml[at0 + (int64_t)i * step] : p.own_ml[at1 + (int64_t)(i - n0) * p.group];
     float m = x.x;
 #pragma unroll
     for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
@@ -541,7 +530,7 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
 #pragma unroll 8
     for (int q = 0; q < k; ++q) {
       const int iq = i0 + q * W;
-      const float* po = iq < n0 ? p.pre_o + (at0 + (int64_t)iq * p.row_tile) * HD : p.own_o + (at1 + (int64_t)(iq - n0) * p.group) * HD;
+      const float* po = iq < n0 ? p.pre_o + (at0 + (int64_t)iq * step) * HD : p.own_o + (at1 + (int64_t)(iq - n0) * p.group) * HD;
       float v[V];
       if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po + lane * 4);
       else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po + lane * 2);
@@ -591,7 +580,7 @@ struct Carve {
   }
 };
 struct Plan {
-  int row_tile, row_tiles;
+  int row_tile, row_tiles, tc_groups;
   size_t sched, pre_blocks, own_blocks, pre_o, pre_ml, own_o, own_ml, total;
 };
 
@@ -602,11 +591,13 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
   w.row_tiles = (rows + w.row_tile - 1) / w.row_tile;
   // a piece more than its predecessor starts a block or a group: at most blocks + groups of them
   const size_t blocks = (size_t)n_sm * kBlocksPerSm;
-  const size_t pre = (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
+  w.tc_groups = (rows + 2 * kTcRows - 1) / (2 * kTcRows);
+  const size_t pre = rows > kTcFrom ? ((size_t)n_sm + (size_t)d.n_kv_heads * w.tc_groups) * 2 * kTcRows
+                                    : (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
   const size_t own = (blocks + (size_t)d.n_kv_heads * d.batch) * group;
   Carve cv;
   w.sched = cv.take(sizeof(int) * (d.batch + 1));
-  w.pre_blocks = cv.take(sizeof(int2) * d.n_kv_heads * w.row_tiles);
+  w.pre_blocks = cv.take(sizeof(int2) * d.n_kv_heads * std::max(w.row_tiles, w.tc_groups));
   w.own_blocks = cv.take(sizeof(int2) * d.n_kv_heads * d.batch);
   w.pre_o = cv.take(pre * d.head_dim * sizeof(float));
   w.pre_ml = cv.take(pre * sizeof(float2));
@@ -617,24 +608,33 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
 }
 
 template <int HD>
-cudaError_t run(AttendParams p, const mk_cache& c, cudaStream_t stream) {
+cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
   const int grid = c.n_sm * kBlocksPerSm;
-  attend_tiles<HD><<<grid, kAttThreads, Layout<HD>::kTotal, stream>>>(p, c.kmap, c.vmap, c.kwhole, c.vwhole);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join's blocks are set up while the tiles are still under way
-  // Few rows: four warps each, since a row then has many pieces; else the SMs are busy with a warp a row.
-  const int64_t rows = (int64_t)c.d.batch * c.d.n_q_heads;
-  const bool few = rows <= 8 * c.n_sm;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
+  cfg.stream = stream;
+  cudaError_t e;
+  if (p.tc) {
+    e = attend_prefix_tc(p, c, stream);
+    if (e != cudaSuccess) return e;
+  }
+  // blocks of the next kernel are set up while this one's are still under way
+  cfg.numAttrs = p.tc;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAttThreads);
+  cfg.dynamicSmemBytes = Layout<HD>::kTotal;
+  e = cudaLaunchKernelEx(&cfg, attend_tiles<HD>, p, c.kmap, c.vmap, c.kwhole, c.vwhole);
+  if (e != cudaSuccess) return e;
+  // Few rows: four warps each, since a row then has many pieces; else the SMs are busy with a warp a row.
+  const int64_t rows = (int64_t)c.d.batch * c.d.n_q_heads;
+  const bool few = rows <= 8 * c.n_sm;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   return few ? cudaLaunchKernelEx(&cfg, attend_join<HD, 4>, p) : cudaLaunchKernelEx(&cfg, attend_join<HD, 1>, p);
 }
 
@@ -644,7 +644,9 @@ size_t attend_workspace(const mk_cache_desc& d, int n_sm) { return plan(d, n_sm)
 
 cudaError_t attend_prepare() {
   static_assert(Layout<64>::kSlots <= 8 && Layout<128>::kSlots <= 8, "barriers of the ring");
-  cudaError_t e = cudaFuncSetAttribute(attend_tiles<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<64>::kTotal);
+  cudaError_t e = attend_prefix_tc_prepare();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attend_tiles<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<64>::kTotal);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attend_tiles<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kTotal);
 }
@@ -663,7 +665,9 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.base = !c.view.bt ? prefix_len : prefix_len / (p.whole ? kTile : c.box) * (p.whole ? kTile : c.box);
   p.row_tile = w.row_tile;
   p.row_tiles = w.row_tiles;
-  p.wide = std::max(p.group, prefix_len ? w.row_tile : 0) > 32;
+  p.tc = prefix_len > 0 && c.d.batch * p.group > kTcFrom;
+  p.tc_groups = w.tc_groups;
+  p.wide = std::max(p.group, prefix_len && !p.tc ? w.row_tile : 0) > 32;
   p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * 1.44269504088896341f;
   p.q = (const uint16_t*)q;
   p.seq_lens = seq_lens;

@@ -1,0 +1,41 @@
+// What the attention kernels share: parameters, workspace layout.
+#pragma once
+
+#include "mk_cache.h"
+
+namespace mk {
+
+constexpr int kTcRows = 128;    // rows of a tensor-core row tile (the M of its products)
+constexpr int kTcTile = 128;    // cache positions of its tiles
+
+struct AttendParams {
+  CacheView c;
+  int layer, group, box;
+  int whole;               // a tile that starts at a multiple of kTile (contiguous: anywhere) is one TMA box
+  int prefix, base;        // own tiles start at base: prefix rounded down so that no box crosses a page
+  int row_tile, row_tiles; // prefix rows per group, row tiles per KV head
+  int wide;                // some piece has more than 32 rows: one query buffer
+  float scale;             // scale * log2 e
+  const uint16_t* q;
+  const int32_t* seq_lens;
+  uint16_t* out;
+  float* lse;
+  int tc, tc_groups;       // the prefix runs in attend_prefix_tc: row groups of two row tiles per KV head
+  // workspace
+  float *pre_o, *own_o;    // [piece][row_tile | group][hd]
+  float2 *pre_ml, *own_ml; // [piece][rows]
+  int2 *pre_blocks, *own_blocks;  // [group] first and last block with a piece of it
+  int* sched;              // [0] whether prefix groups have pieces, [1...] own tiles of each sequence
+};
+
+// Blocks that work, and the first unit of cost of block i of G.
+__device__ __forceinline__ int active_blocks(int64_t cost, int grid) { return (int)min(cost, (int64_t)grid); }
+__device__ __forceinline__ int64_t first_unit(int64_t cost, int i, int G) { return cost * i / G; }
+
+// Attention over the prefix with tcgen05 (mk_attend_tc.cu): leaves its pieces
+// in pre_o / pre_ml as entries of kTcRows rows, two a piece, and the blocks of
+// every group in pre_blocks.
+cudaError_t attend_prefix_tc_prepare();
+cudaError_t attend_prefix_tc(const AttendParams& p, const mk_cache& c, cudaStream_t stream);
+
+}  // namespace mk

@@ -16,10 +16,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // Maps of a cache or pool (rows of head_dim elements), 128-byte swizzle
-// (16-byte chunk c of row r at c ^ (r & 7)).  Small boxes: 64 columns x
-// box_rows rows.  Whole boxes: all columns x kWholeRows rows, which land as
+// (16-byte chunk c of row r at c ^ (r & 7)).  Small and tall boxes: 64 columns
+// x so many rows.  Whole boxes: all columns x kWholeRows rows, which land as
 // [64-column block][row].
-cudaError_t encode_maps(const void* base, int64_t rows, int hd, int box_rows, CUtensorMap* small, CUtensorMap* whole) {
+cudaError_t encode_maps(const void* base, int64_t rows, int hd, int small_rows, int tall_rows, CUtensorMap* small,
+                        CUtensorMap* tall, CUtensorMap* whole) {
   void* p = nullptr;
   cudaDriverEntryPointQueryResult q;
   if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
@@ -28,7 +29,7 @@ cudaError_t encode_maps(const void* base, int64_t rows, int hd, int box_rows, CU
   const auto encode = reinterpret_cast<EncodeTiledFn>(p);
   const cuuint64_t dims2[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
   const cuuint64_t strides2[1] = {(cuuint64_t)hd * 2};
-  const cuuint32_t box2[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t box2[2] = {64, (cuuint32_t)small_rows};
   const cuuint64_t dims3[3] = {64, (cuuint64_t)rows, (cuuint64_t)(hd / 64)};
   const cuuint64_t strides3[2] = {(cuuint64_t)hd * 2, 128};
   const cuuint32_t box3[3] = {64, (cuuint32_t)kWholeRows, (cuuint32_t)(hd / 64)};
@@ -36,6 +37,11 @@ cudaError_t encode_maps(const void* base, int64_t rows, int hd, int box_rows, CU
   CUresult r = encode(small, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims2, strides2, box2, ones,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  box2[1] = (cuuint32_t)tall_rows;
+  if (r == CUDA_SUCCESS)
+    r = encode(tall, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims2, strides2, box2, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r == CUDA_SUCCESS)
     r = encode(whole, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims3, strides3, box3, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -129,9 +135,10 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
   c->n_sm = n_sm;
   c->k = (uint16_t*)kv->k;
   c->v = (uint16_t*)kv->v;
-  c->box = mk::cache_box_rows(kv->block_table ? kv->page_size : 0);
-  cudaError_t e = mk::encode_maps(kv->k, rows, d.head_dim, c->box, &c->kmap, &c->kwhole);
-  if (e == cudaSuccess) e = mk::encode_maps(kv->v, rows, d.head_dim, c->box, &c->vmap, &c->vwhole);
+  c->box = mk::cache_box_rows(kv->block_table ? kv->page_size : 0, 32);
+  c->tall = mk::cache_box_rows(kv->block_table ? kv->page_size : 0, 128);
+  cudaError_t e = mk::encode_maps(kv->k, rows, d.head_dim, c->box, c->tall, &c->kmap, &c->ktall, &c->kwhole);
+  if (e == cudaSuccess) e = mk::encode_maps(kv->v, rows, d.head_dim, c->box, c->tall, &c->vmap, &c->vtall, &c->vwhole);
   if (e != cudaSuccess) {
     delete c;
     return e == cudaErrorInvalidValue ? MK_ERR_UNSUPPORTED : MK_ERR_CUDA;

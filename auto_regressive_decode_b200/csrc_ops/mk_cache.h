@@ -39,11 +39,10 @@ struct CacheView {
   __device__ __forceinline__ int64_t head_pitch() const { return bt ? page : T; }
 };
 
-// Rows of a small TMA box of the cache: it lies in one page.
-inline int cache_box_rows(int page) {
-  if (!page) return 32;
-  int r = 32;
-  while (page % r) r /= 2;
+// Rows of a TMA box of the cache, at most `most` (a power of two): it lies in one page.
+inline int cache_box_rows(int page, int most) {
+  int r = most;
+  while (page % r) r /= 2;  // a contiguous cache (page 0): the most
   return r;
 }
 
@@ -82,9 +81,10 @@ struct mk_cache {
   mk_cache_desc d;
   mk::CacheView view;
   uint16_t *k, *v;
-  int device, n_sm, box;
+  int device, n_sm, box, tall;
   float2* rope;  // [max_ctx][hd/2] (cos, sin)
   CUtensorMap kmap, vmap;      // boxes of 64 columns x box rows
   CUtensorMap kwhole, vwhole;  // boxes of all columns x kWholeRows rows
+  CUtensorMap ktall, vtall;    // boxes of 64 columns x tall rows
   void* region;
 };
