@@ -7,10 +7,12 @@
 // other's warpgroup computes.  More than 128 rows: the streams are two row tiles that read
 // the same K and V tiles.  Fewer: they are the even and the odd tiles of the same rows.
 //
-//   warps 0-3, 4-7  softmax of stream 0, 1: S from tensor memory, maximum and
-//                   sum of the row, P = 2^(s - m) as bf16 over S's columns
-//   warp 8          one thread issues the products
-//   warp 9          TMA of K and V tiles into a ring
+//   warps 0-7, 8-15 softmax of stream 0, 1, two threads a row (half the columns
+//                   each): S from tensor memory, maximum and sum of the row, P =
+//                   2^(s - m) as bf16 over S's columns
+//   warp 16         one thread issues the products
+//   warp 17         TMA of K and V tiles into a ring
+//   warps 18, 19    nothing: they fill the warpgroup that gives its registers to the softmax
 //
 // A row's reference m is raised, and its output scaled, only when a score
 // exceeds it by kSlack (log2): p stays below 2^kSlack, far inside fp32 and
@@ -22,6 +24,8 @@
 // Bound: the tensor cores (4 head_dim flops a row and position) and, nearly as
 // much, the exponentials (16 a clock and SM: 128 x 128 of them last as long as the
 // tile's two products); with up to about 128 rows, the cache's bytes.
+#include <type_traits>
+
 #include "mk_attend.h"
 #include "mk_ptx.h"
 
@@ -30,24 +34,34 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSoftmaxThreads = 256;
-constexpr int kTcThreads = kSoftmaxThreads + 64;
+constexpr int kSoftmaxThreads = 512;  // two a row of each stream
+constexpr int kTcThreads = kSoftmaxThreads + 128;
+// Registers a thread: the compiler's share of the launch (96 at 640 threads), then split.
+constexpr int kRegsFew = 64, kRegsMany = 104;
+static_assert(kRegsFew * 128 + kRegsMany * kSoftmaxThreads <= 96 * kTcThreads, "the launch's registers");
+constexpr int kHalf = kTcTile / 2;  // positions of a thread's half row
 constexpr float kSlack = 8.f;
 constexpr int kTcHead = 1;  // tiles that a group's start and end count as
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <int HD>
 struct TcLayout {
   static constexpr int kSlotBytes = kTcTile * HD * 2;       // K or V tile: [HD/64][128 rows][128 B], swizzled
   static constexpr int kSlots = 128 * 1024 / kSlotBytes;
   static constexpr int kQ = kSlots * kSlotBytes;            // two query tiles, laid out the same
   static constexpr int kQBytes = kTcRows * HD * 2;
-  static constexpr int kCtl = kQ + 2 * kQBytes;
+  static constexpr int kSwap = kQ + 2 * kQBytes;             // float[stream][turn][half][128]
+  static constexpr int kCtl = kSwap + 2 * 2 * 2 * 128 * 4;
   static constexpr int kTotal = kCtl + 512 + 1024;          // 1024: aligned by hand
 };
 
 struct TcCtl {
   unsigned long long full[8], empty[8];
-  unsigned long long q_full, s_full[2], p_full[2], o_done[2];
+  unsigned long long q_full, tail, s_full[2], p_full[2], o_done[2];  // [stream]
   uint32_t tmem;
   int dead, max_len;
 };
@@ -85,8 +99,8 @@ struct Walk {
 
 // The order in which a piece's 2 n tiles of K and V pass through the ring: as
 // the products want them.  Pair: K0 V0 K1 V1 ...; else K0 K1 V0 K2 V1 K3 V2 ...
-__device__ __forceinline__ int k_place(const Piece& a, int t) { return a.pair ? 2 * t : (t ? 2 * t - 1 : 0); }
-__device__ __forceinline__ int v_place(const Piece& a, int t) { return a.pair ? 2 * t + 1 : min(2 * t + 2, 2 * a.n - 1); }
+__device__ __forceinline__ int k_place(bool pair, int t) { return pair ? 2 * t : (t ? 2 * t - 1 : 0); }
+__device__ __forceinline__ int v_place(bool pair, int t, int n) { return pair ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
 
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -100,15 +114,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = smem_addr(smem);
   TcCtl* ctl = reinterpret_cast<TcCtl*>(smem + S::kCtl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const CacheView& c = p.c;
+  const CacheView& cv = p.c;
   volatile int* dead = &ctl->dead;
 
   if (tid == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);
-      mbar_init(smem_addr(&ctl->empty[s]), 1);
+      mbar_init(smem_addr(&ctl->empty[s]), 2);
     }
     mbar_init(smem_addr(&ctl->q_full), kSoftmaxThreads);
+    mbar_init(smem_addr(&ctl->tail), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&ctl->s_full[s]), 1);
       mbar_init(smem_addr(&ctl->p_full[s]), kSoftmaxThreads / 2);
@@ -118,11 +133,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     ctl->max_len = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(smem_addr(&ctl->tmem), 512);
+  if (warp == 16) tmem_alloc(smem_addr(&ctl->tmem), 512);
   __syncthreads();
   grid_launch_next();
   int longest = 0;
-  for (int b = tid; b < c.B; b += kTcThreads) longest = max(longest, min(__ldg(p.seq_lens + b), c.T));
+  for (int b = tid; b < cv.B; b += kTcThreads) longest = max(longest, min(__ldg(p.seq_lens + b), cv.T));
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) atomicMax(&ctl->max_len, longest);
   tc_fence_before();
@@ -132,13 +147,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int tiles = (prefix_end + kTcTile - 1) / kTcTile;
-  const int64_t cost = tiles ? (int64_t)(tiles + kTcHead) * p.tc_groups * c.nkv : 0;
+  const int64_t cost = tiles ? (int64_t)(tiles + kTcHead) * p.tc_groups * cv.nkv : 0;
   const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
-  Walk walk{tiles, p.tc_groups, c.B * p.group, 0, 0};
+  Walk walk{tiles, p.tc_groups, cv.B * p.group, 0, 0};
   if (cta < G) walk.u = first_unit(cost, cta, G), walk.end = first_unit(cost, cta + 1, G);
   Piece a;
 
-  if (warp == 9) {  // ---- TMA: K and V tiles in the order of k_place, v_place
+  const int whole_tiles = prefix_end / kTcTile;
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 17) {  // ---- TMA: K and V tiles in the order of k_place, v_place
     uint32_t slot = 0, phase = 0;
     const int boxes = kTcTile / tall, cb = lane / boxes, j = lane % boxes;  // this lane's box of a tile
     while (walk.next(a)) {
@@ -156,8 +174,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool wanted = cb < CB && at < prefix_end;
         bool ok = true;
         int row = 0;
-        if (wanted) row = (int)(c.row(p.layer, 0, at, &ok) + a.kvh * c.head_pitch());
-        if (!ok) set_status(c.status, MK_ERR_RANGE, 0);
+        if (wanted) row = (int)(cv.row(p.layer, 0, at, &ok) + a.kvh * cv.head_pitch());
+        if (!ok) set_status(cv.status, MK_ERR_RANGE, 0);
         const uint32_t full = smem_addr(&ctl->full[slot]);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * tall * 128;
         mbar_wait(smem_addr(&ctl->empty[slot]), phase ^ 1, dead);
@@ -168,6 +186,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tma_box2(base + slot * S::kSlotBytes + cb * (kTcTile * 128) + j * tall * 128, is_k ? &kmap : &vmap, cb * 64, row, full);
         }
         __syncwarp();
+        if (!is_k && a.t0 + t == whole_tiles) {
+          // the prefix ends in this tile: what lies behind is anything, and 0 x NaN is NaN
+          const int have = prefix_end - whole_tiles * kTcTile;
+          const uint32_t v = base + slot * S::kSlotBytes;
+          mbar_wait(full, phase, dead);
+          for (int e = lane; e < (kTcTile - have) * 8 * CB; e += 32) {
+            const int chunk = e % 8, block = e / 8 % CB, r = have + e / (8 * CB);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + block * (kTcTile * 128) + r * 128 + chunk * 16), "r"(0) : "memory");
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl->tail));
+        }
         if (++slot == S::kSlots) slot = 0, phase ^= 1;
       }
     }
@@ -176,94 +207,110 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int s = 0; s < S::kSlots; ++s)
         while (!mbar_try(smem_addr(&ctl->full[s]), (uint32_t)s < slot ? phase : phase ^ 1) && globaltimer() - t0 < 20000000ull) {
         }
-      if (lane == 0) set_status(c.status, MK_ERR_DEVICE_TIMEOUT, cta);
+      if (lane == 0) set_status(cv.status, MK_ERR_DEVICE_TIMEOUT, cta);
     }
-  } else if (warp == 8) {  // ---- products
+  } else if (warp == 16) {  // ---- products
     constexpr uint32_t kQk = mma_desc(kTcRows, kTcTile, false), kPv = mma_desc(kTcRows, HD, true);
+    const uint32_t leader = lane == 0;
+    const uint64_t q_desc = smem_desc(base + S::kQ, 16, 1024), k_desc = smem_desc(base, 16, 1024),
+                   v_desc = smem_desc(base, kTcTile * 128, 1024);
     uint32_t at = 0;  // tiles that passed through the ring in earlier pieces
-    uint32_t q_phase = 0, p_phase[2] = {0, 0};
+    uint32_t q_phase = 0, tail_phase = 0, p_phase0 = 0, p_phase1 = 0;
     while (walk.next(a)) {
-      const int n0 = a.pair ? a.n : (a.n + 1) / 2, n1 = a.pair ? a.n : a.n / 2;
       mbar_wait(smem_addr(&ctl->q_full), q_phase, dead);
       q_phase ^= 1;
-      tc_fence_after();
-      auto slot_of = [&](int place) { return (at + place) % S::kSlots; };
-      auto wait_full = [&](int place) { mbar_wait(smem_addr(&ctl->full[slot_of(place)]), (at + place) / S::kSlots & 1, dead); };
-      auto qk = [&](int s, int i) {  // scores of the stream's tile i
-        const int place = k_place(a, a.pair ? i : 2 * i + s);
-        wait_full(place);
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t q = base + S::kQ + (a.pair ? s : 0) * S::kQBytes, k = base + slot_of(place) * S::kSlotBytes;
+      // The products of a piece.  What stands between two runs of them is kept short: a
+      // product is issued as the matrix unit takes it (65 to 71 clocks each), and the unit
+      // idles meanwhile; a commit costs it 40 to 75.  So one commit a stream and tile tells
+      // the softmax that its scores are there, that the product before is done (in order of
+      // issue) and, through the softmax, the ring that the tiles have been read.
+      auto products = [&](auto pair_) {
+        constexpr bool kPair = decltype(pair_)::value;
+        const int n0 = kPair ? a.n : (a.n + 1) / 2, n1 = kPair ? a.n : a.n / 2;
+        auto qk = [&](auto s_, int i) {  // scores of the stream's tile i
+          constexpr int s = decltype(s_)::value;
+          const uint32_t place = at + k_place(kPair, kPair ? i : 2 * i + s), slot = place % S::kSlots;
+          if (!kPair || s == 0) mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
+          const uint64_t q = q_desc + (kPair ? s : 0) * (S::kQBytes >> 4), k = k_desc + slot * (S::kSlotBytes >> 4);
 #pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks) {
-            const uint32_t off = ks / 4 * (128 * 128) + ks % 4 * 32;
-            tc_mma_ss(tmem + kS + s * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kQk, ks > 0);
+          for (int ks = 0; ks < HD / 16; ++ks) {  // 16 columns are 32 bytes of a swizzled line; 4 k-steps a 64-column block
+            constexpr uint32_t kBlock = kTcRows * 128 >> 4;
+            const uint32_t off = ks / 4 * kBlock + ks % 4 * 2;
+            tc_mma_ss(tmem + kS + s * 128, q + off, k + off, kQk, ks > 0, leader);
           }
-          tc_commit(smem_addr(&ctl->s_full[s]));
-          if (!a.pair || s == 1) tc_commit(smem_addr(&ctl->empty[slot_of(place)]));
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int s, int i) {
-        const int t = a.pair ? i : 2 * i + s, place = v_place(a, t);
-        mbar_wait(smem_addr(&ctl->p_full[s]), p_phase[s], dead);
-        p_phase[s] ^= 1;
-        wait_full(place);
-        const uint32_t v = base + slot_of(place) * S::kSlotBytes;
-        const int have = prefix_end - (a.t0 + t) * kTcTile;
-        if (have < kTcTile && (!a.pair || s == 0)) {
-          // the prefix ends in this tile: what lies behind is anything, and 0 x NaN is NaN
-          for (int e = lane; e < (kTcTile - have) * 8 * CB; e += 32) {
-            const int chunk = e % 8, cb = e / 8 % CB, r = have + e / (8 * CB);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + cb * (kTcTile * 128) + r * 128 + chunk * 16), "r"(0) : "memory");
+          tc_commit(smem_addr(&ctl->s_full[s]), leader);
+        };
+        auto pv = [&](auto s_, int i, int n, uint32_t& p_phase) {
+          constexpr int s = decltype(s_)::value;
+          const int t = kPair ? i : 2 * i + s;
+          const uint32_t place = at + v_place(kPair, t, a.n), slot = place % S::kSlots;
+          if (!kPair || s == 0) {
+            mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
+            if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail), tail_phase, dead);
           }
-          fence_async_shared();
-          __syncwarp();
-        }
-        tc_fence_after();
-        if (lane == 0) {
+          const uint64_t v = v_desc + slot * (S::kSlotBytes >> 4);
+          constexpr uint32_t kD = kO + s * 128, kP = kS + s * 128;
+          mbar_wait(smem_addr(&ctl->p_full[s]), p_phase, dead);
+          p_phase ^= 1;
+          tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < kTcTile / 16; ++ks)
-            tc_mma_ts(tmem + kO + s * 128, tmem + kS + s * 128 + ks * 8, smem_desc(v + ks * 2048, kTcTile * 128, 1024), kPv, i > 0 || ks > 0);
-          tc_commit(smem_addr(&ctl->o_done[s]));
-          if (!a.pair || s == 1) tc_commit(smem_addr(&ctl->empty[slot_of(place)]));
+          for (int ks = 0; ks < kTcTile / 16; ++ks)  // 16 lines on
+            tc_mma_ts(tmem + kD, tmem + kP + ks * 8, v + ks * (16 * 128 >> 4), kPv, ks > 0 || i > 0, leader);
+          if (i + 1 == n) tc_commit(smem_addr(&ctl->o_done[s]), leader);
+        };
+        const std::integral_constant<int, 0> s0;
+        const std::integral_constant<int, 1> s1;
+        // A stream's next scores overwrite its probabilities: after the product that reads them, in order of issue.
+        qk(s0, 0);
+        if (n1) qk(s1, 0);
+        for (int i = 0; i < n0; ++i) {
+          pv(s0, i, n0, p_phase0);
+          if (i + 1 < n0) qk(s0, i + 1);
+          if (i < n1) pv(s1, i, n1, p_phase1);
+          if (i + 1 < n1) qk(s1, i + 1);
         }
-        __syncwarp();
       };
-      qk(0, 0);
-      if (n1) qk(1, 0);
-      for (int i = 0; i < n0; ++i) {
-        pv(0, i);
-        if (i + 1 < n0) qk(0, i + 1);
-        if (i < n1) pv(1, i);
-        if (i + 1 < n1) qk(1, i + 1);
-      }
+      if (a.pair) products(std::true_type());
+      else products(std::false_type());
+      if (a.t0 + a.n > whole_tiles) tail_phase ^= 1;
       at += 2 * a.n;
     }
+  }
   } else {  // ---- softmax of stream s
-    const int s = warp / 4, r = tid % 128;  // row of the stream's tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    const int s = warp / 8, c = warp / 4 % 2, r = tid % 128;  // half c of row r of the stream's tile
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;
-    const uint32_t s_at = tmem + lanes + kS + s * 128, o_at = tmem + lanes + kO + s * 128;
+    const uint32_t s_at = tmem + lanes + kS + s * 128, o_at = tmem + lanes + kO + s * 128 + c * (HD / 2);
     const float scale = fabsf(p.scale);
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the query's signs
-    uint32_t q_phase = 0, s_phase = 0, o_phase = 0;
+    float* swap = reinterpret_cast<float*>(smem + S::kSwap) + s * 512;  // [turn][half][row]
+    auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + s * 4 + warp % 4) : "memory"); };
+    uint32_t q_phase = 0, s_phase = 0, o_phase = 0, at = 0, turn = 0;
+    // The other half's value for this row.
+    auto other = [&](float mine) {
+      float* w = swap + turn * 256;
+      turn ^= 1;
+      w[c * 128 + r] = mine;
+      pair_bar();
+      return w[(c ^ 1) * 128 + r];
+    };
     while (walk.next(a)) {
       const int n = a.pair ? a.n : (a.n + 1 - s) / 2;
       const int row = (a.pair ? s * kTcRows : 0) + r;
       const bool valid = row < a.rows;
       const int b = (a.row0 + row) / p.group, head = a.kvh * p.group + (a.row0 + row) % p.group;
       const int lim = valid ? min(__ldg(p.seq_lens + b), prefix_end) : 0;
-      if (a.pair || s == 0) {  // the row's query, swizzled as TMA would
-        const uint4* q = reinterpret_cast<const uint4*>(p.q + ((int64_t)b * c.nq + head) * HD);
-        uint4 x[HD / 8];
+      if (a.pair || s == 0) {  // half of the row's query, swizzled as TMA would
+        const uint4* q = reinterpret_cast<const uint4*>(p.q + ((int64_t)b * cv.nq + head) * HD) + c * (HD / 16);
+        uint4 x[HD / 16];
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) x[i] = valid ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        uint8_t* at = smem + S::kQ + (a.pair ? s : 0) * S::kQBytes + r * 128;
+        for (int i = 0; i < HD / 16; ++i) x[i] = valid ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+        uint8_t* to = smem + S::kQ + (a.pair ? s : 0) * S::kQBytes + r * 128;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
+        for (int i = 0; i < HD / 16; ++i) {
+          const int ch = c * (HD / 16) + i;
           x[i].x ^= flip; x[i].y ^= flip; x[i].z ^= flip; x[i].w ^= flip;
-          *reinterpret_cast<uint4*>(at + i / 8 * (kTcRows * 128) + (((i % 8) ^ (r & 7)) << 4)) = x[i];
+          *reinterpret_cast<uint4*>(to + ch / 8 * (kTcRows * 128) + (((ch % 8) ^ (r & 7)) << 4)) = x[i];
         }
         fence_async_shared();
       }
@@ -275,65 +322,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
-        const int t0 = (a.t0 + (a.pair ? i : 2 * i + s)) * kTcTile;
+        const int t = a.pair ? i : 2 * i + s, t0 = (a.t0 + t) * kTcTile + c * kHalf;
         mbar_wait(smem_addr(&ctl->s_full[s]), s_phase, dead);
         s_phase ^= 1;
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x + q * 32);
+        if (r == 0 && c == 0) {  // the scores' K tile has been read, and the V tile of the product before
+          const uint32_t uses = a.pair ? 1 : 2;
+          mbar_arrive(smem_addr(&ctl->empty[(at + k_place(a.pair, t)) % S::kSlots]), uses);
+          if (i) mbar_arrive(smem_addr(&ctl->empty[(at + v_place(a.pair, a.pair ? t - 1 : t - 2, a.n)) % S::kSlots]), uses);
+        }
+        uint32_t x[kHalf];
+        tmem_ld32(s_at + c * kHalf, x);
+        tmem_ld32(s_at + c * kHalf + 32, x + 32);
         tmem_wait_ld();
-        if (__any_sync(0xffffffffu, t0 + kTcTile > lim)) {
+        if (__any_sync(0xffffffffu, t0 + kHalf > lim)) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
+          for (int e = 0; e < kHalf; ++e)
             if (t0 + e >= lim) x[e] = 0xff800000u;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; e += 4) {
+        for (int e = 0; e < kHalf; e += 8) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[e + q]));
+          for (int q = 0; q < 4; ++q) mx[q] = max3_nan(mx[q], __uint_as_float(x[e + q]), __uint_as_float(x[e + q + 4]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        const bool raise = top > m + kSlack || (m == -INFINITY && top > m);
+        float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale;
+        const float twin = other(top);  // also: both halves have read their scores before probabilities cover them
+        top = max3_nan(top, twin, twin);
+        if (top == INFINITY) top = NAN;  // a NaN or an infinite score leaves nothing but NaN of the row
+        const bool raise = !(top <= m + kSlack);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? ex2(m - top) : 1.f;
           if (raise) m = top;
           l *= f;
-          if (i > 0) {  // the stream's output so far, once its last product is done
-            mbar_wait(smem_addr(&ctl->o_done[s]), o_phase ^ 1, dead);
-            tc_fence_after();
+          if (i > 0) {  // half of the stream's output so far: its last product was done before these scores
 #pragma unroll 1
             for (int q = 0; q < HD / 32; ++q) {
-              uint32_t y[32];
-              tmem_ld32(o_at + q * 32, y);
+              uint32_t y[16];
+              tmem_ld16(o_at + q * 16, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-              tmem_st32(o_at + q * 32, y);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tmem_st16(o_at + q * 16, y);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const F2 scale2 = pack2(scale, scale), back2 = pack2(-ref, -ref);
+        F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * e]), scale, -ref));
-            const float p1 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * e + 1]), scale, -ref));
-            sum[e & 1] += p0;
-            sum[2 + (e & 1)] += p1;
+            const F2 d = fma2(pack2(__uint_as_float(x[q * 32 + 2 * e]), __uint_as_float(x[q * 32 + 2 * e + 1])), scale2, back2);
+            float d0, d1;
+            unpack2(d, d0, d1);
+            const float p0 = ex2(d0), p1 = ex2(d1);
+            sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
             y[e] = pack_bf16x2(p0, p1);  // the operand of the second product, as the cache is
           }
-          tmem_st16(s_at + q * 16, y);
+          tmem_st16(s_at + c * (kHalf / 2) + q * 16, y);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float u0, u1;
+        unpack2(add2(sum[0], sum[1]), u0, u1);
+        l += u0 + u1;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_addr(&ctl->p_full[s]));
-        o_phase ^= 1;
       }
       // leave the piece
       const int64_t entry = ((int64_t)cta + a.gidx) * 2 + s;
@@ -341,27 +397,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (a.first) p.pre_blocks[a.gidx].x = cta;
         if (a.last) p.pre_blocks[a.gidx].y = cta;
       }
-      if (valid) p.pre_ml[entry * kTcRows + r] = make_float2(m, l);
+      l += other(l);
+      if (valid && c == 0) p.pre_ml[entry * kTcRows + r] = make_float2(m, l);
       if (n) {
-        mbar_wait(smem_addr(&ctl->o_done[s]), o_phase ^ 1, dead);
+        mbar_wait(smem_addr(&ctl->o_done[s]), o_phase, dead);
+        o_phase ^= 1;
         tc_fence_after();
-        float* out = p.pre_o + (entry * kTcRows + r) * HD;
+        if (r == 0 && c == 0)
+          mbar_arrive(smem_addr(&ctl->empty[(at + v_place(a.pair, a.pair ? n - 1 : 2 * n - 2 + s, a.n)) % S::kSlots]), a.pair ? 1 : 2);
+        float* out = p.pre_o + (entry * kTcRows + r) * HD + c * (HD / 2);
 #pragma unroll 1
         for (int q = 0; q < HD / 32; ++q) {
-          uint32_t y[32];
-          tmem_ld32(o_at + q * 32, y);
+          uint32_t y[16];
+          tmem_ld16(o_at + q * 16, y);
           tmem_wait_ld();
           if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(out + q * 32 + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + q * 16 + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           }
         }
       }
+      at += 2 * a.n;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }

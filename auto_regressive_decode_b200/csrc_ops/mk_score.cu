@@ -64,30 +64,6 @@ struct Sum {
   float m, z, s;
 };
 
-// Two fp32 values in one register pair (sm_100 add / mul / fma.rn.f32x2).
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 pack(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // The logits of one 16-byte vector, and their maximum (NaN ignored).
 template <typename T>
 struct Vec;
@@ -378,25 +354,25 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       const float top = Vec<T>::top(raw);
       most = fmaxf(most, top);
       if (top > lifted) acc.lift(top, lifted);
-      F2 z2 = pack(0.f, 0.f), s2 = z2;
-      const F2 back = pack(-acc.c, -acc.c), scale = pack(kLog2e, kLog2e);
+      F2 z2 = pack2(0.f, 0.f), s2 = z2;
+      const F2 back = pack2(-acc.c, -acc.c), scale = pack2(kLog2e, kLog2e);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float f[VEC];
         Vec<T>::get(raw[u], f);
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-          const F2 d = fma2(pack(f[i], f[i + 1]), scale, back);
+          const F2 d = fma2(pack2(f[i], f[i + 1]), scale, back);
           float d0, d1;
-          unpack(d, d0, d1);
-          const F2 e = pack(ex2(d0), ex2(d1));
+          unpack2(d, d0, d1);
+          const F2 e = pack2(ex2(d0), ex2(d1));
           z2 = add2(z2, e);
           s2 = fma2(e, d, s2);
         }
       }
       float z0, z1, s0, s1;
-      unpack(z2, z0, z1);
-      unpack(s2, s0, s1);
+      unpack2(z2, z0, z1);
+      unpack2(s2, s0, s1);
       float z = z0 + z1, s = s0 + s1;
       if (!(s == s) || acc.huge) {
         // 0 * -infinity (masked logits), a real NaN, or a reference too large for the fma:
