@@ -15,8 +15,13 @@
 // with scores in units of log2 (scale * log2 e folded into one factor).
 //
 // Bound: memory, 4 head_dim bytes of cache a position and KV head against
-// 4 head_dim flops a row.  A producer warp keeps a ring of TMA boxes in flight;
-// two small blocks an SM, so that one streams while the other starts or ends a piece.
+// 4 head_dim flops a row, and for short sequences the latency of a piece's start
+// and end.  A producer warp keeps a ring of TMA boxes in flight; two or three small
+// blocks an SM, so that one streams while the others start or end a piece.
+//
+// Up to 8 rows (NARROW) are the N of the products, S^T = K Q^T and O^T = V^T P^T;
+// more are their M, 16 at a time.  As M, 8 rows would take twice the products and
+// registers, and two blocks an SM instead of three.
 #include <algorithm>
 
 #include "mk_attend.h"
@@ -31,24 +36,27 @@ constexpr int kTile = 64;                        // cache positions a tile
 constexpr int kWarps = 4;                        // compute warps; the next one is the producer
 constexpr int kComputeThreads = kWarps * 32;
 constexpr int kAttThreads = kComputeThreads + 32;
-constexpr int kBlocksPerSm = 2;
 constexpr int kHead = 2;                         // tiles that a group's start and end count as
 constexpr int kMaxRows = 64;                     // rows of a prefix row tile
 constexpr int kTcFrom = 16;                      // more rows of a KV head than this share a prefix: tensor-core kernel
-constexpr int kRedPitch = 64 + 4;                // floats a row of the joining buffer (64 columns at a time)
 
-template <int HD>
+template <int HD, bool NARROW>
 struct Layout {
+  static constexpr int kBlocksPerSm = NARROW ? 3 : 2;
   static constexpr int kSlotBytes = kTile * HD * 2;         // one tile of K or of V: [HD/64][kTile rows][128 B], swizzled
-  static constexpr int kSlots = 64 * 1024 / kSlotBytes;
-  static constexpr int kRed = kSlots * kSlotBytes;          // float[kWarps][16][kRedPitch]
+  static constexpr int kSlots = (NARROW ? 48 : 64) * 1024 / kSlotBytes;
+  static constexpr int kCols = NARROW ? HD : 64;            // columns joined at a time
+  static constexpr int kRedRows = NARROW ? 8 : 16;
+  static constexpr int kRedPitch = kCols + 4;               // floats a row of the joining buffer
+  static constexpr int kRed = kSlots * kSlotBytes;          // float[kWarps][kRedRows][kRedPitch]
+  static constexpr int kQRows = NARROW ? 8 : 32;            // rows of a query buffer; there are two
   static constexpr int kQPitch = HD * 2 + 16;               // bytes a query row: ldmatrix rows in different banks
-  static constexpr int kQ = kRed + kWarps * 16 * kRedPitch * 4;  // two buffers of 32 rows, or one of 64
-  static constexpr int kMl = kQ + kMaxRows * kQPitch;       // float2[kWarps][16]
-  static constexpr int kCum = kMl + kWarps * 16 * 8;        // int[kCacheMaxBatch + 1]: cost of the sequences before
-  static constexpr int kCtl = kCum + (kCacheMaxBatch + 4) * 4;
-  static constexpr int kTotal = kCtl + 256 + 1024;          // 1024: the ring is aligned by hand
-  static_assert(kTotal <= 113 * 1024, "two blocks an SM");
+  static constexpr int kQ = kRed + kWarps * kRedRows * kRedPitch * 4;
+  static constexpr int kMl = kQ + 2 * kQRows * kQPitch;     // float2[kWarps][16]
+  static constexpr int kCtl = kMl + kWarps * 16 * 8;
+  static constexpr int kLens = kCtl + 256;                  // int[batch], then int[batch + 1]: cost of the sequences before
+  static constexpr int total(int batch) { return kLens + (2 * batch + 1) * 4 + 1024; }  // 1024: the ring is aligned by hand
+  static_assert(kLens + 2048 + 1024 <= 227 * 1024 / kBlocksPerSm - 1024, "blocks an SM");
 };
 
 struct Ctl {
@@ -71,48 +79,73 @@ struct Piece {
   bool last;          // it ends its group
 };
 
+// The pieces of a block's run [u, end) of the groups' costs: found once, then
+// group after group (a division is slow next to a short piece).
 struct Walk {
   const AttendParams& p;
   const int* cum;
-  int pre_tiles, pre_groups;
-  int64_t u, end;
-  __device__ Walk(const AttendParams& prm, const int* cumulative, int pre, int64_t u0, int64_t u1)
-      : p(prm), cum(cumulative), pre_tiles(pre), pre_groups(pre ? prm.c.nkv * prm.row_tiles : 0), u(u0), end(u1) {}
+  int pre_tiles, u, end;
+  bool shared;
+  int g, kvh, b, n, r;  // the group: prefix group or sequence and KV head; its cost, the run's place in it
+  __device__ Walk(const AttendParams& prm, const int* cumulative, int pre, int u0, int u1)
+      : p(prm), cum(cumulative), pre_tiles(pre), u(u0), end(u1) {
+    const int pre_cost = pre ? pre + kHead : 0, groups = p.c.nkv * p.row_tiles, shared_cost = groups * pre_cost;
+    shared = u < shared_cost;
+    if (shared) {
+      g = u / pre_cost;
+      r = u - g * pre_cost;
+      n = pre_cost;
+      kvh = g / p.row_tiles;
+      b = 0;
+    } else {
+      const int v = u - shared_cost, w = v / p.c.nkv;
+      int lo = 0, hi = p.c.B;  // the sequence with cum[b] <= w < cum[b + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cum[mid] <= w) lo = mid; else hi = mid;
+      }
+      b = lo;
+      n = max(cum[b + 1] - cum[b], 1);
+      const int at = v - cum[b] * p.c.nkv;
+      kvh = at / n;
+      r = at - kvh * n;
+      g = b * p.c.nkv + kvh;
+    }
+  }
   __device__ __forceinline__ bool next(Piece& a) {
     while (u < end) {
-      const int pre_cost = pre_tiles + kHead;
-      const int64_t shared_cost = (int64_t)pre_groups * pre_cost;
-      int n, r;  // cost of the group, place in it
-      if (u < shared_cost) {
-        a.shared = true;
-        a.gidx = (int)(u / pre_cost);
-        r = (int)(u % pre_cost);
-        a.kvh = a.gidx / p.row_tiles;
-        a.tile0 = a.gidx % p.row_tiles * p.row_tile;
-        a.b = 0;
-        n = pre_cost;
-      } else {
-        const int64_t v = u - shared_cost;
-        const int w = (int)(v / p.c.nkv);
-        int lo = 0, hi = p.c.B;  // the sequence with cum[b] <= w < cum[b + 1]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (cum[mid] <= w) lo = mid; else hi = mid;
+      if (r == n) {  // the next group
+        r = 0;
+        ++g;
+        if (shared) {
+          if (g < p.c.nkv * p.row_tiles) {
+            kvh = g / p.row_tiles;
+          } else {
+            shared = false;
+            g = kvh = 0;
+            b = 0;
+            n = cum[1];
+          }
+        } else if (++kvh == p.c.nkv) {
+          kvh = 0;
+          ++b;
         }
-        n = cum[lo + 1] - cum[lo];
-        const int at = (int)(v - (int64_t)cum[lo] * p.c.nkv);
-        a.shared = false;
-        a.b = lo;
-        a.kvh = at / n;
-        r = at % n;
-        a.tile0 = 0;
-        a.gidx = lo * p.c.nkv + a.kvh;
+        while (!shared && (n = cum[b + 1] - cum[b]) == 0) {  // sequences without tiles; u < end: one follows
+          ++b;
+          g += p.c.nkv;
+        }
       }
-      const int take = (int)min((int64_t)(n - r), end - u);
-      u += take;
+      const int take = min(n - r, end - u);
+      a.shared = shared;
+      a.gidx = g;
+      a.kvh = kvh;
+      a.b = b;
+      a.tile0 = shared ? g % p.row_tiles * p.row_tile : 0;
       a.i0 = max(r - kHead, 0);
       a.i1 = r + take - kHead;
-      a.last = r + take == n;
+      u += take;
+      r += take;
+      a.last = r == n;
       if (a.i1 > a.i0) return true;
     }
     return false;
@@ -123,26 +156,26 @@ __device__ __forceinline__ int piece_rows(const AttendParams& p, const Piece& a)
   return a.shared ? min(p.row_tile, p.c.B * p.group - a.tile0) : p.group;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
+template <int HD, bool NARROW>
+__global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
     attend_tiles(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kwhole,
                  const __grid_constant__ CUtensorMap vwhole) {
-  using S = Layout<HD>;
+  using S = Layout<HD, NARROW>;
   constexpr int KS = HD / 16;  // k-steps of the score product
-  constexpr int NT = HD / 8;   // column tiles of the output
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   const uint32_t ring = smem_addr(smem);
   float* red = reinterpret_cast<float*>(smem + S::kRed);
   float2* sml = reinterpret_cast<float2*>(smem + S::kMl);
-  int* cum = reinterpret_cast<int*>(smem + S::kCum);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + S::kCtl);
+  int* lens = reinterpret_cast<int*>(smem + S::kLens);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const CacheView& c = p.c;
+  int* cum = lens + c.B;
   volatile int* dead = &ctl->dead;
 
-  if (tid == 0) {
+  if (tid == kAttThreads - 1) {
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);
       mbar_init(smem_addr(&ctl->empty[s]), kWarps);
@@ -152,33 +185,21 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
       mbar_init(smem_addr(&ctl->qempty[s]), kWarps);
     }
     ctl->dead = 0;
-    ctl->max_len = 0;
     fence_mbar_init();
   }
   grid_launch_next();
-  // Lengths, and the cost of the sequences before each: a warp takes 32 at a
-  // time; with more, they are scanned once all have been read.
-  auto length = [&](int b) {
-    const int n = __ldg(p.seq_lens + b);
-    return n < 0 ? 0 : min(n, c.T);
-  };
-  __syncthreads();
-  int longest = 0;
   for (int b = tid; b < c.B; b += kAttThreads) {
     const int n = __ldg(p.seq_lens + b), m = n < 0 ? 0 : min(n, c.T);
     if (n != m && blockIdx.x == 0) set_status(c.status, MK_ERR_RANGE, b);
-    const int t = own_tiles(p, m);
-    cum[b + 1] = t ? t + kHead : 0;
-    longest = max(longest, m);
+    lens[b] = m;
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) atomicMax(&ctl->max_len, longest);
   __syncthreads();
-  if (warp == 0) {
-    int sum = 0;
+  if (warp == 0) {  // the cost of the sequences before each, and the longest
+    int sum = 0, longest = 0;
     for (int b0 = 0; b0 < c.B; b0 += 32) {
-      const int b = b0 + lane;
-      int x = b < c.B ? cum[b + 1] : 0;
+      const int b = b0 + lane, m = b < c.B ? lens[b] : 0, t = own_tiles(p, m), cost = t ? t + kHead : 0;
+      longest = max(longest, m);
+      int x = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -187,13 +208,17 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
       if (b < c.B) cum[b + 1] = sum + x;
       sum += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) cum[0] = 0;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      cum[0] = 0;
+      ctl->max_len = longest;
+    }
   }
   __syncthreads();
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int pre_tiles = p.tc ? 0 : (prefix_end + kTile - 1) / kTile;
-  const int64_t cost = (pre_tiles ? (int64_t)(pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + (int64_t)cum[c.B] * c.nkv;
+  const int cost = (pre_tiles ? (pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + cum[c.B] * c.nkv;
   if (blockIdx.x == 0) {
     for (int b = tid; b < c.B; b += kAttThreads) p.sched[1 + b] = cum[b + 1] - cum[b];
     if (tid == 0) p.sched[0] = prefix_end;
@@ -227,12 +252,12 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
       if (!walk.next(a)) return false;
       start = a.shared ? 0 : p.base;
       lo = a.shared ? 0 : p.prefix;
-      hi = a.shared ? prefix_end : length(a.b);
+      hi = a.shared ? prefix_end : lens[a.b];
       i = a.i0;
       place();
       // its query rows
       const int rows = piece_rows(p, a);
-      const uint32_t full = smem_addr(&ctl->qfull[qbuf]), dst = ring + S::kQ + qbuf * 32 * S::kQPitch;
+      const uint32_t full = smem_addr(&ctl->qfull[qbuf]), dst = ring + S::kQ + qbuf * S::kQRows * S::kQPitch;
       mbar_wait(smem_addr(&ctl->qempty[qbuf]), qphase ^ 1, dead);
       if (!__any_sync(0xffffffffu, *dead)) {
         if (lane == 0) mbar_expect_tx(full, rows * HD * 2);
@@ -289,36 +314,52 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
     return;
   }
 
-  // ---- compute warps: rows as the mma's M (16 a row block), warps = row blocks x position splits
+  // ---- compute warps
   uint32_t slot = 0, phase = 0, qbuf = 0, qphase = 0;
-  const int gq = lane / 4, cq = lane % 4;
+  const int gq = lane / 4, cq = lane % 4, mi = lane >> 3;
   while (walk.next(a)) {
     const int rows = piece_rows(p, a);
-    const int R = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);  // row blocks
-    const int rb = warp % R, sp = warp / R;
     const int lo = a.shared ? 0 : p.prefix, start = a.shared ? 0 : p.base;
-    const int hi = a.shared ? prefix_end : length(a.b);
-    int lim[2];  // positions of this lane's two rows end here
+    const int hi = a.shared ? prefix_end : lens[a.b];
+    // row blocks of 16 (or the one of 8); a warp has row block rb and of every tile the 16-position slices sp * R + ...
+    const int R = NARROW || rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), rb = warp % R, sp = warp / R;
+    // this lane's two rows: columns of S^T, or rows of S; their positions end at lim
+    const int row0 = NARROW ? 2 * cq : rb * 16 + gq, row1 = NARROW ? 2 * cq + 1 : rb * 16 + gq + 8;
+    int lim[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = rb * 16 + gq + 8 * h;
-      lim[h] = r >= rows ? 0 : (a.shared ? min(length((a.tile0 + r) / p.group), hi) : hi);
+      const int r = h ? row1 : row0;
+      lim[h] = r >= rows ? 0 : (a.shared ? min(lens[(a.tile0 + r) / p.group], hi) : hi);
     }
-    uint32_t qf[KS][4];
+    constexpr int kQRegs = NARROW ? 2 : 4;
+    uint32_t qf[KS][kQRegs];
     mbar_wait(smem_addr(&ctl->qfull[qbuf]), qphase, dead);
     {
-      const uint32_t at = ring + S::kQ + (qbuf * 32 + rb * 16 + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
+      const uint32_t buf = ring + S::kQ + qbuf * S::kQRows * S::kQPitch;
+      if constexpr (NARROW) {  // B fragments: rows 0-7, 32 columns at a time
+        const uint32_t at = buf + (lane & 7) * S::kQPitch + mi * 16;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) ldmatrix_x4(qf[k], at + k * 32);
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t f[4];
+          ldmatrix_x4(f, at + k * 32);
+          qf[k][0] = f[0]; qf[k][1] = f[1]; qf[k + 1][0] = f[2]; qf[k + 1][1] = f[3];
+        }
+      } else {  // A fragments
+        const uint32_t at = buf + (rb * 16 + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) ldmatrix_x4(qf[k], at + k * 32);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&ctl->qempty[qbuf]));
     if (p.wide || qbuf) qphase ^= 1;
     qbuf = p.wide ? 0 : qbuf ^ 1;
 
-    float o[NT][4];
+    // the output: HD columns of this lane's two rows (S::kTiles fragments of 4)
+    constexpr int kTiles = NARROW ? HD / 16 : HD / 8;
+    float o[kTiles][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < kTiles; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     for (int i = a.i0; i < a.i1; ++i) {
@@ -331,85 +372,102 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
       const int t0 = start + i * kTile;
       mbar_wait(kfull, kphase, dead);
       bool have_v = false;
-      for (int js = 0; js < R; ++js) {  // 16-position slices of this warp: sp * R + js
+      for (int js = 0; js < R; ++js) {
         const int s0 = (sp * R + js) * 16, p0 = t0 + s0;
-        if (p0 < hi && p0 + 16 > lo) {
-          float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // odd k-steps: shorter chains
-          {
-            const int mi = lane >> 3, row = s0 + (mi >> 1) * 8 + (lane & 7);
+        if (p0 >= hi || p0 + 16 <= lo) continue;
+        // scores, e = 0..3 of two 8-wide parts: value [part][e], its position and row
+        constexpr int kParts = NARROW ? 1 : 2;
+        float s[kParts][4], u[kParts][4];  // u: odd k-steps (shorter chains)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              const int ch = k * 2 + (mi & 1);
-              uint32_t f[4];
-              ldmatrix_x4(f, kslot + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-              mma16816(k & 1 ? u[0] : s[0], qf[k], f[0], f[1]);
-              mma16816(k & 1 ? u[1] : s[1], qf[k], f[2], f[3]);
-            }
+        for (int n = 0; n < kParts; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = u[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int ch = k * 2 + (NARROW ? lane >> 4 : mi & 1), row = s0 + (NARROW ? lane & 15 : (mi >> 1) * 8 + (lane & 7));
+          uint32_t f[4];
+          ldmatrix_x4(f, kslot + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+          if constexpr (NARROW) {
+            mma16816(k & 1 ? u[0] : s[0], f, qf[k][0], qf[k][1]);
+          } else {
+            mma16816(k & 1 ? u[0] : s[0], qf[k], f[0], f[1]);
+            mma16816(k & 1 ? u[1] : s[1], qf[k], f[2], f[3]);
           }
-          // mask, maximum
-          float mx[2] = {-INFINITY, -INFINITY};
+        }
+        // mask, maximum of the lane's two rows
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kParts; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int pos = p0 + n * 8 + cq * 2 + (e & 1);
-              s[n][e] = pos >= lo && pos < lim[e >> 1] ? (s[n][e] + u[n][e]) * p.scale : -INFINITY;
-              mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-            }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            mx[h] = fmaxf(mx[h], m[h]);
-          }
-          const bool grew = mx[0] > m[0] || mx[1] > m[1];
-          float ref[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) ref[h] = mx[h] == -INFINITY ? 0.f : mx[h];
-          if (__any_sync(0xffffffffu, grew)) {
-            const float f0 = ex2(m[0] - ref[0]), f1 = ex2(m[1] - ref[1]);
-            l[0] *= f0;
-            l[1] *= f1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              o[n][0] *= f0;
-              o[n][1] *= f0;
-              o[n][2] *= f1;
-              o[n][3] *= f1;
-            }
-            m[0] = mx[0];
-            m[1] = mx[1];
+          for (int e = 0; e < 4; ++e) {
+            const int pos = NARROW ? p0 + gq + (e >> 1) * 8 : p0 + n * 8 + cq * 2 + (e & 1), h = NARROW ? e & 1 : e >> 1;
+            s[n][e] = pos >= lo && pos < lim[h] ? (s[n][e] + u[n][e]) * p.scale : -INFINITY;
+            mx[h] = fmaxf(mx[h], s[n][e]);
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[n][e] = ex2(s[n][e] - ref[e >> 1]);
-              l[e >> 1] += s[n][e];
-            }
-          // probabilities as the A operand of the second product: rounded to bf16, as the cache is
-          const uint32_t pf[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                                  pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
-          if (!have_v) {
-            mbar_wait(vfull, vphase, dead);
-            have_v = true;
-          }
-          // rows outside [lo, hi) hold anything, and 0 x NaN is NaN: clear them in the fragment
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (p0 < lo || p0 + 16 > hi) {
-            const int q0 = p0 + cq * 2;
-            keep0 = (q0 >= lo && q0 < hi ? 0xffffu : 0u) | (q0 + 1 >= lo && q0 + 1 < hi ? 0xffff0000u : 0u);
-            keep1 = (q0 + 8 >= lo && q0 + 8 < hi ? 0xffffu : 0u) | (q0 + 9 >= lo && q0 + 9 < hi ? 0xffff0000u : 0u);
-          }
-          const int mi = lane >> 3, row = s0 + (mi & 1) * 8 + (lane & 7);
+          for (int x = NARROW ? 4 : 1; x < (NARROW ? 32 : 4); x <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], x));
+          mx[h] = fmaxf(mx[h], m[h]);
+        }
+        const bool grew = mx[0] > m[0] || mx[1] > m[1];
+        float ref[2];
 #pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            const int ch = n + (mi >> 1);
-            uint32_t f[4];
-            ldmatrix_x4_trans(f, vslot + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-            mma16816(o[n], pf, f[0] & keep0, f[1] & keep1);
-            mma16816(o[n + 1], pf, f[2] & keep0, f[3] & keep1);
+        for (int h = 0; h < 2; ++h) ref[h] = mx[h] == -INFINITY ? 0.f : mx[h];
+        if (__any_sync(0xffffffffu, grew)) {
+          const float f[2] = {ex2(m[0] - ref[0]), ex2(m[1] - ref[1])};
+          l[0] *= f[0];
+          l[1] *= f[1];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] *= f[NARROW ? e & 1 : e >> 1];
+          m[0] = mx[0];
+          m[1] = mx[1];
+        }
+#pragma unroll
+        for (int n = 0; n < kParts; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int h = NARROW ? e & 1 : e >> 1;
+            s[n][e] = ex2(s[n][e] - ref[h]);
+            l[h] += s[n][e];
+          }
+        // probabilities as an operand of the second product: rounded to bf16, as the cache is
+        uint32_t pf[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]), 0, 0};
+        if constexpr (NARROW) {  // [position][row] to B's [row][position]
+          pf[0] = movmatrix(pf[0]);
+          pf[1] = movmatrix(pf[1]);
+        } else {
+          pf[2] = pack_bf16x2(s[1][0], s[1][1]);
+          pf[3] = pack_bf16x2(s[1][2], s[1][3]);
+        }
+        if (!have_v) {
+          mbar_wait(vfull, vphase, dead);
+          have_v = true;
+        }
+        // rows outside [lo, hi) hold anything, and 0 x NaN is NaN: clear them in the fragment
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (p0 < lo || p0 + 16 > hi) {
+          const int q0 = p0 + cq * 2;
+          keep0 = (q0 >= lo && q0 < hi ? 0xffffu : 0u) | (q0 + 1 >= lo && q0 + 1 < hi ? 0xffff0000u : 0u);
+          keep1 = (q0 + 8 >= lo && q0 + 8 < hi ? 0xffffu : 0u) | (q0 + 9 >= lo && q0 + 9 < hi ? 0xffff0000u : 0u);
+        }
+        const int row = s0 + (NARROW ? mi >> 1 : mi & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int n = 0; n < HD / 16; ++n) {  // 16 columns at a time
+          const int ch = 2 * n + (NARROW ? mi & 1 : mi >> 1);
+          uint32_t f[4];
+          ldmatrix_x4_trans(f, vslot + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+          if constexpr (NARROW) {
+            f[0] &= keep0;
+            f[1] &= keep0;
+            f[2] &= keep1;
+            f[3] &= keep1;
+            mma16816(o[n], f, pf[0], pf[1]);
+          } else {
+            mma16816(o[2 * n], pf, f[0] & keep0, f[1] & keep1);
+            mma16816(o[2 * n + 1], pf, f[2] & keep0, f[3] & keep1);
           }
         }
       }
@@ -424,54 +482,56 @@ __global__ void __launch_bounds__(kAttThreads, kBlocksPerSm)
     // ---- join the position splits of each row block and leave the piece in the workspace
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (cq == 0) sml[warp * 16 + gq + 8 * h] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int x = NARROW ? 4 : 1; x < (NARROW ? 32 : 4); x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+      if ((NARROW ? gq : cq) == 0) sml[warp * 16 + (h ? row1 : row0) % 16] = make_float2(m[h], l[h]);
     }
-    compute_bar();
     const int64_t pid = (int64_t)cta + a.gidx;
+    const int stride = a.shared ? p.row_tile : p.group;
+    float* po = (a.shared ? p.pre_o : p.own_o) + pid * stride * HD;
+    float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * stride;
     if (tid == 0) {
       int2* at = (a.shared ? p.pre_blocks : p.own_blocks) + a.gidx;
       if (a.i0 == 0) at->x = cta;
       if (a.last) at->y = cta;
     }
-    const int stride = a.shared ? p.row_tile : p.group;
-    float* po = (a.shared ? p.pre_o : p.own_o) + pid * stride * HD;
-    float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * stride;
-    float f[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = gq + 8 * h;
-      float M = -INFINITY, L = 0.f;
-      for (int w = rb; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + r].x);
-      f[h] = M == -INFINITY ? 0.f : ex2(m[h] - M);
-      if (sp == 0 && cq == 0 && rb * 16 + r < rows) {
-        for (int w = rb; w < kWarps; w += R) {
-          const float2 x = sml[w * 16 + r];
-          if (x.y != 0.f) L += x.y * ex2(x.x - M);
+    for (int part = 0; part < HD / S::kCols; ++part) {
+      if (part) compute_bar();
+      if constexpr (NARROW) {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          float* d = red + (warp * 8 + 2 * cq) * S::kRedPitch + n * 16 + gq;
+          if (row0 < rows) d[0] = o[n][0], d[8] = o[n][2];
+          if (row1 < rows) d[S::kRedPitch] = o[n][1], d[S::kRedPitch + 8] = o[n][3];
         }
-        pml[rb * 16 + r] = make_float2(M, L);
-      }
-    }
+      } else {
 #pragma unroll
-    for (int half = 0; half < HD / 64; ++half) {
-      if (half) compute_bar();
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float* v = o[half * 8 + n];
-        float* d = red + (warp * 16 + gq) * kRedPitch + n * 8 + cq * 2;
-        if (rb * 16 + gq < rows) *reinterpret_cast<float2*>(d) = make_float2(v[0] * f[0], v[1] * f[0]);
-        if (rb * 16 + gq + 8 < rows) *reinterpret_cast<float2*>(d + 8 * kRedPitch) = make_float2(v[2] * f[1], v[3] * f[1]);
+        for (int n = 0; n < 8; ++n) {
+          const float* v = o[part * 8 + n];
+          float* d = red + (warp * 16 + gq) * S::kRedPitch + n * 8 + cq * 2;
+          if (row0 < rows) *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
+          if (row1 < rows) *reinterpret_cast<float2*>(d + 8 * S::kRedPitch) = make_float2(v[2], v[3]);
+        }
       }
       compute_bar();
-      for (int e = tid; e < rows * 16; e += kComputeThreads) {
-        const int r = e / 16, col = e % 16 * 4;
+      constexpr int kQuads = S::kCols / 4;
+      for (int e = tid; e < rows * kQuads; e += kComputeThreads) {
+        const int r = e / kQuads, col = e % kQuads * 4;
+        float M = -INFINITY, L = 0.f;
+        for (int w = r / 16; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + r % 16].x);
+        const float to = M == -INFINITY ? 0.f : M;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = r / 16; w < kWarps; w += R) {
-          const float4 x = *reinterpret_cast<const float4*>(red + (w * 16 + r % 16) * kRedPitch + col);
-          sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+          const float2 ml = sml[w * 16 + r % 16];
+          const float4 x = *reinterpret_cast<const float4*>(red + (w * S::kRedRows + r % 16) * S::kRedPitch + col);
+          if (ml.y == 0.f) continue;  // every position masked (a NaN sum is passed on)
+          const float f = ex2(ml.x - to);
+          L += f * ml.y;
+          sum.x += f * x.x; sum.y += f * x.y; sum.z += f * x.z; sum.w += f * x.w;
         }
-        *reinterpret_cast<float4*>(po + (int64_t)r * HD + half * 64 + col) = sum;
+        *reinterpret_cast<float4*>(po + (int64_t)r * HD + part * S::kCols + col) = sum;
+        if (part == 0 && col == 0) pml[r] = make_float2(M, L);
       }
     }
     compute_bar();  // sml and red are free for the next piece
@@ -590,7 +650,7 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
   w.row_tile = std::min((rows + 15) / 16 * 16, kMaxRows);
   w.row_tiles = (rows + w.row_tile - 1) / w.row_tile;
   // a piece more than its predecessor starts a block or a group: at most blocks + groups of them
-  const size_t blocks = (size_t)n_sm * kBlocksPerSm;
+  const size_t blocks = (size_t)n_sm * 3;
   w.tc_groups = (rows + 2 * kTcRows - 1) / (2 * kTcRows);
   const size_t pre = rows > kTcFrom ? ((size_t)n_sm + (size_t)d.n_kv_heads * w.tc_groups) * 2 * kTcRows
                                     : (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
@@ -607,9 +667,11 @@ Plan plan(const mk_cache_desc& d, int n_sm) {
   return w;
 }
 
-template <int HD>
+template <int HD, bool NARROW>
 cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
-  const int grid = c.n_sm * kBlocksPerSm;
+  using S = Layout<HD, NARROW>;
+  const int smem = S::total(c.d.batch);
+  const int grid = c.n_sm * std::min(S::kBlocksPerSm, 228 * 1024 / (smem + 1024));  // all of them resident
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -625,8 +687,8 @@ cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
   cfg.numAttrs = p.tc;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kAttThreads);
-  cfg.dynamicSmemBytes = Layout<HD>::kTotal;
-  e = cudaLaunchKernelEx(&cfg, attend_tiles<HD>, p, c.kmap, c.vmap, c.kwhole, c.vwhole);
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, attend_tiles<HD, NARROW>, p, c.kmap, c.vmap, c.kwhole, c.vwhole);
   if (e != cudaSuccess) return e;
   // Few rows: four warps each, since a row then has many pieces; else the SMs are busy with a warp a row.
   const int64_t rows = (int64_t)c.d.batch * c.d.n_q_heads;
@@ -642,13 +704,20 @@ cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
 
 size_t attend_workspace(const mk_cache_desc& d, int n_sm) { return plan(d, n_sm).total; }
 
+template <int HD, bool NARROW>
+cudaError_t allow_smem() {
+  static_assert(Layout<HD, NARROW>::kSlots <= 8, "barriers of the ring");
+  return cudaFuncSetAttribute(attend_tiles<HD, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<HD, NARROW>::total(kCacheMaxBatch));
+}
+
 cudaError_t attend_prepare() {
-  static_assert(Layout<64>::kSlots <= 8 && Layout<128>::kSlots <= 8, "barriers of the ring");
   cudaError_t e = attend_prefix_tc_prepare();
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(attend_tiles<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<64>::kTotal);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attend_tiles<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kTotal);
+  if (e == cudaSuccess) e = allow_smem<64, false>();
+  if (e == cudaSuccess) e = allow_smem<64, true>();
+  if (e == cudaSuccess) e = allow_smem<128, false>();
+  if (e == cudaSuccess) e = allow_smem<128, true>();
+  return e;
 }
 
 cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* seq_lens, int prefix_len, float scale,
@@ -680,7 +749,9 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.pre_ml = (float2*)(ws + w.pre_ml);
   p.own_o = (float*)(ws + w.own_o);
   p.own_ml = (float2*)(ws + w.own_ml);
-  return c.d.head_dim == 128 ? run<128>(p, c, stream) : run<64>(p, c, stream);
+  const bool narrow = std::max(p.group, prefix_len && !p.tc ? c.d.batch * p.group : 0) <= 8;
+  if (c.d.head_dim == 128) return narrow ? run<128, true>(p, c, stream) : run<128, false>(p, c, stream);
+  return narrow ? run<64, true>(p, c, stream) : run<64, false>(p, c, stream);
 }
 
 }  // namespace mk

@@ -28,9 +28,12 @@ struct AttendParams {
   int* sched;              // [0] whether prefix groups have pieces, [1...] own tiles of each sequence
 };
 
-// Blocks that work, and the first unit of cost of block i of G.
-__device__ __forceinline__ int active_blocks(int64_t cost, int grid) { return (int)min(cost, (int64_t)grid); }
-__device__ __forceinline__ int64_t first_unit(int64_t cost, int i, int G) { return cost * i / G; }
+// Blocks that work, and the first unit of cost of block i of G (G is below 2^15).
+__device__ __forceinline__ int active_blocks(int cost, int grid) { return min(cost, grid); }
+__device__ __forceinline__ int first_unit(int cost, int i, int G) {
+  const int q = cost / G;
+  return q * i + (cost - q * G) * i / G;
+}
 
 // Attention over the prefix with tcgen05 (mk_attend_tc.cu): leaves its pieces
 // in pre_o / pre_ml as entries of kTcRows rows, two a piece, and the blocks of

@@ -76,12 +76,12 @@ struct Piece {
 
 struct Walk {
   int tiles, groups, total_rows;
-  int64_t u, end;
+  int u, end;
   __device__ __forceinline__ bool next(Piece& a) {
     while (u < end) {
       const int n = tiles + kTcHead;
-      a.gidx = (int)(u / n);
-      const int r = (int)(u % n), take = (int)min((int64_t)(n - r), end - u);
+      a.gidx = u / n;
+      const int r = u % n, take = min(n - r, end - u);
       u += take;
       a.kvh = a.gidx / groups;
       a.row0 = a.gidx % groups * 2 * kTcRows;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int tiles = (prefix_end + kTcTile - 1) / kTcTile;
-  const int64_t cost = tiles ? (int64_t)(tiles + kTcHead) * p.tc_groups * cv.nkv : 0;
+  const int cost = tiles ? (tiles + kTcHead) * p.tc_groups * cv.nkv : 0;
   const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
   Walk walk{tiles, p.tc_groups, cv.B * p.group, 0, 0};
   if (cta < G) walk.u = first_unit(cost, cta, G), walk.end = first_unit(cost, cta + 1, G);

@@ -115,6 +115,9 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
     if (rows >= limit) return MK_ERR_UNSUPPORTED;
   }
 
+  // the attention's schedule counts tiles of 64 positions, for every sequence and KV head, in 32 bits
+  if (((int64_t)d.max_ctx / 64 + 4) * d.n_kv_heads * d.batch >= limit) return MK_ERR_UNSUPPORTED;
+
   int dev = 0, n_sm = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||

@@ -115,6 +115,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t a[4], uint32_t saddr)
                : "memory");
 }
 
+// Transpose of an 8x8 b16 matrix held a pair a lane (lane 4 r + c: row r, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // ---- tcgen05: tensor memory and its matrix unit ----------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {  // a whole warp; the base address goes to `slot`
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(columns) : "memory");

@@ -247,7 +247,8 @@ typedef struct mk_cache mk_cache;
  * Returns MK_ERR_UNSUPPORTED for head_dim not 64 or 128, more than 64 query
  * heads per KV head or a number that n_kv_heads does not divide, batch above
  * 1024, a page_size that is not a multiple of 16, caches of 2^31 rows
- * (head_dim elements each) or more, misaligned pointers (16 bytes), and
+ * (head_dim elements each) or more, batch * n_kv_heads * max_ctx / 64 of 2^31 or
+ * more, misaligned pointers (16 bytes), and
  * MK_ERR_INVALID_ARG for malformed sizes.  The caches and the block table are
  * borrowed.
  */
