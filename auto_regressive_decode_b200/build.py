@@ -1,9 +1,10 @@
-"""Build libmk.so (the decode megakernel and its C ABI) in-tree with nvcc for sm_100a."""
+"""Build libmk.so (the kernels and their C ABI, nvcc for sm_100a) and _mk_torch.so (the operators' torch binding) in-tree."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -14,6 +15,8 @@ HEADERS = ["mk_internal.h", "mk_device.h"]
 OPS = os.path.join(HERE, "csrc_ops")
 OPS_SOURCES = ["mk_cache.cu", "mk_append.cu", "mk_attend.cu", "mk_attend_tc.cu", "mk_score.cu"]
 OPS_HEADERS = ["mk_attend.h", "mk_cache.h", "mk_ptx.h"]
+BIND = os.path.join(HERE, "_mk_torch.so")
+BIND_SOURCE = os.path.join(OPS, "mk_torch.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-Xcompiler", "-fPIC",
          "-shared", "-cudart", "static"]
@@ -25,21 +28,46 @@ def _inputs():
         [os.path.join(root, "include", "mk.h")]
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(target, inputs) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(f) > t for f in inputs)
+
+
+def stale() -> bool:
+    return _older(LIB, _inputs())
+
+
+def _run_into(target, cmd):
+    """Run `cmd` with an -o file beside the target, then put it in the target's place."""
+    tmp = target + f".tmp{os.getpid()}"
+    subprocess.check_call([*cmd, "-o", tmp], cwd=CSRC)
+    os.replace(tmp, target)
+
+
+def build_binding(force: bool = False) -> str:
+    """The operators' torch binding: plain C++ against torch's headers, linked with libmk.so beside it."""
+    root = os.path.dirname(HERE)
+    inputs = [BIND_SOURCE, os.path.join(OPS, "mk_cache.h"), os.path.join(root, "include", "mk.h")]
+    if not force and not _older(BIND, inputs):
+        return BIND
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    lib = os.path.join(base, "lib")
+    _run_into(BIND, [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BIND_SOURCE, *[f"-I{d}" for d in inc],
+                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-L{HERE}", "-l:libmk.so", f"-L{lib}",
+                     "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])
+    return BIND
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, *(["-Xptxas", "-v"] if verbose else []), "-o", tmp,
-           *[os.path.join(CSRC, f) for f in SOURCES], *[os.path.join(OPS, f) for f in OPS_SOURCES]]
-    subprocess.check_call(cmd, cwd=CSRC)
-    os.replace(tmp, LIB)
+    if force or stale():
+        _run_into(LIB, [NVCC, *FLAGS, *(["-Xptxas", "-v"] if verbose else []), *[os.path.join(CSRC, f) for f in SOURCES],
+                        *[os.path.join(OPS, f) for f in OPS_SOURCES]])
+    build_binding(force)
     return LIB
 
 

@@ -24,6 +24,7 @@ struct CacheView {
   int bt_stride, page, n_pages;
   int* status;  // [0] code, [1] detail
 
+#ifdef __CUDACC__
   // Row index of (layer, sequence, KV head 0, position); a KV head adds head_pitch() rows.
   // A page outside the pool is recorded and read as page 0 (*ok = false).
   __device__ __forceinline__ int64_t row(int layer, int b, int pos, bool* ok) const {
@@ -37,6 +38,7 @@ struct CacheView {
     return ((int64_t)layer * B + b) * nkv * T + pos;
   }
   __device__ __forceinline__ int64_t head_pitch() const { return bt ? page : T; }
+#endif
 };
 
 // Rows of a TMA box of the cache, at most `most` (a power of two): it lies in one page.

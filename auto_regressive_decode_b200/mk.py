@@ -343,37 +343,22 @@ class Decoder:
 
 # ---- operators on the KV cache, and scores of tokens ----------------------------------------------
 
-# The checks below build their messages only when they fail, and ask torch for the raw stream: a call on a
-# few tokens is as long as its host side.
+_torch_calls = None
+
+
+def _calls():
+    """The operators' torch binding (_mk_torch.so): checks tensors, allocates results, calls libmk.so."""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch  # noqa: F401  (its libraries first)
+        from . import _mk_torch
+        _mk_torch.set_error(MkError)
+        _torch_calls = _mk_torch
+    return _torch_calls
+
 
 def _refuse(what):
     raise MkError(MK_ERR_INVALID_ARG, what)
-
-
-def _float_dtype(t, what):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return MK_DTYPE_BF16
-    if t.dtype is torch.float32:
-        return MK_DTYPE_FP32
-    _refuse(f"{what}: bf16 or fp32 is wanted, got {t.dtype}")
-
-
-def _raw_stream(index, stream):
-    """cudaStream_t of `stream`, or of the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _empty(shape, dtype, device, stream):
-    """Uninitialised tensor of the stream that is going to write it."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class Cache:
@@ -381,8 +366,8 @@ class Cache:
 
     k, v: device bf16 [L][B][n_kv][max_ctx][hd], or with block_table (device int32
     [B][ceil(max_ctx/page_size)]) page pools [L][n_pages][n_kv][page_size][hd]; page_size a multiple of 16.
-    Calls are asynchronous; tensors must stay alive until the stream has used them, and they and the stream
-    belong to the cache's device, which need not be the current one."""
+    Calls are asynchronous on `stream`, or the current stream of the cache's device; that need not be the current
+    device.  A tensor that another stream made must stay alive until the call's stream has used it."""
 
     def __init__(self, k, v, n_q_heads, batch, max_ctx, block_table=None, page_size=0, rope_theta=1e4, rms_eps=1e-6):
         import torch
@@ -391,11 +376,7 @@ class Cache:
                 v.device == k.device and k.is_contiguous() and v.is_contiguous()):
             _refuse("Cache: k and v are contiguous bf16 device tensors of one shape [.][.][.][.][.]")
         L, n, nkv, rows, hd = k.shape
-        self.device, self._index = k.device, k.device.index
-        self.n_layers, self.batch, self.max_ctx = L, batch, max_ctx
-        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, nkv, hd
-        self._q_shape, self._lse_shape = (batch, n_q_heads, hd), (batch, n_q_heads)
-        self._lens_shape, self._starts_shape = (batch,), (batch + 1,)
+        self.device = k.device
         if block_table is None:
             if n != batch or rows != max_ctx:
                 _refuse(f"Cache: k of shape [L][{batch}][n_kv][{max_ctx}][hd] is wanted")
@@ -403,97 +384,47 @@ class Cache:
         else:
             if rows != page_size or page_size <= 0:
                 _refuse(f"Cache: k of shape [L][n_pages][n_kv][{page_size}][hd] is wanted")
-            table = self._ints(block_table, (batch, -(-max_ctx // page_size)), "Cache: block_table")
-            kv = mk_kv(k.data_ptr(), v.data_ptr(), table, page_size, n)
+            shape = (batch, -(-max_ctx // page_size))
+            if not (block_table.dtype == torch.int32 and block_table.shape == shape and block_table.device == k.device and
+                    block_table.is_contiguous()):
+                _refuse(f"Cache: a contiguous int32 block_table of shape {shape} on {k.device} is wanted")
+            kv = mk_kv(k.data_ptr(), v.data_ptr(), block_table.data_ptr(), page_size, n)
         self._keep = (k, v, block_table)
         desc = mk_cache_desc(L, batch, n_q_heads, nkv, hd, max_ctx, rms_eps, rope_theta)
         h = _P()
         with torch.cuda.device(self.device):
             check(mk_cache_create(ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(h)), "mk_cache_create")
-        self.h = h
-        self._ws_bytes = mk_cache_attend_bytes(h)
-
-    def _ints(self, t, shape, what):
-        if t.dtype is self.torch.int32 and t.shape == shape and t.device == self.device and t.is_contiguous():
-            return t.data_ptr()
-        _refuse(f"{what}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
-
-    def _buffer(self, t, shape, dtype, what):
-        if t.dtype is dtype and t.shape == shape and t.device == self.device and t.is_contiguous():
-            return t.data_ptr()
-        _refuse(f"{what}: a contiguous tensor of shape {tuple(shape)}, {dtype}, on {self.device} is wanted")
-
-    def _rows(self, t, shape, dtype, what):
-        """Pointer and token stride of [n][heads][hd] whose heads are contiguous within a token."""
-        if t.shape == shape and t.dtype is dtype and t.device == self.device:
-            s0, s1, s2 = t.stride()
-            if s2 == 1 and (s1 == shape[2] or shape[1] == 1) or shape[0] == 0:
-                return t.data_ptr(), s0
-        _refuse(f"append: {what} of shape {shape}, {dtype}, heads contiguous, on {self.device} is wanted")
+        self.h = h.value
+        self._call = _calls()
+        self.workspace_bytes = mk_cache_attend_bytes(h)
 
     def append(self, layer, k, v, seq_lens, q=None, starts=None, positions=None, q_norm=None, k_norm=None, q_out=None,
                stream=None):
         """Append keys and values (bf16 or fp32 [n][n_kv][hd]) to the cache, the keys rotated; returns the rotated
         q (bf16 [n][n_q][hd]) where q is given.  seq_lens int32 [B]: rows held before; starts int32 [B + 1]: the
         tokens of each sequence (None: one each); see mk_cache_append."""
-        bf16, hd = self.torch.bfloat16, self.head_dim
-        n, dt = k.shape[0], k.dtype
-        code = _float_dtype(k, "append")
-        kv_shape = (n, self.n_kv_heads, hd)
-        kp, ks = self._rows(k, kv_shape, dt, "k")
-        vp, vs = self._rows(v, kv_shape, dt, "v")
-        qp = qs = qop = 0
-        if q is not None:
-            q_shape = (n, self.n_q_heads, hd)
-            qp, qs = self._rows(q, q_shape, dt, "q")
-            if q_out is None:
-                q_out = _empty(q_shape, bf16, self.device, stream)
-                qop = q_out.data_ptr()
-            else:
-                qop = self._buffer(q_out, q_shape, bf16, "append: q_out")
-        elif q_out is not None:
-            _refuse("append: q_out without q")
-        if starts is None and n != self.batch:
-            _refuse(f"append: {self.batch} tokens are wanted without starts")
-        a = mk_append_args(
-            qp, kp, vp, qs, ks, vs,
-            None if starts is None else self._ints(starts, self._starts_shape, "append: starts"),
-            self._ints(seq_lens, self._lens_shape, "append: seq_lens"),
-            None if positions is None else self._ints(positions, (n,), "append: positions"),
-            None if q_norm is None else self._buffer(q_norm, (hd,), bf16, "append: q_norm"),
-            None if k_norm is None else self._buffer(k_norm, (hd,), bf16, "append: k_norm"), qop, n, code)
-        check(mk_cache_append(self.h, layer, a, _raw_stream(self._index, stream)), "mk_cache_append")
-        return q_out
+        if stream is not None:
+            with self.torch.cuda.stream(stream):
+                return self._call.append(self.h, layer, k, v, seq_lens, q, starts, positions, q_norm, k_norm, q_out)
+        return self._call.append(self.h, layer, k, v, seq_lens, q, starts, positions, q_norm, k_norm, q_out)
 
     def attend(self, layer, q, seq_lens, prefix_len=0, scale=0.0, out=None, lse=None, workspace=None, stream=None):
         """Attention of one query token a sequence, q bf16 [B][n_q][hd], over the first seq_lens[b] rows; the rows
         below prefix_len are sequence 0's for all.  Returns (out bf16 [B][n_q][hd], lse fp32 [B][n_q]); see
         mk_cache_attend."""
-        torch, dev, shape = self.torch, self.device, self._q_shape
-        qp = self._buffer(q, shape, torch.bfloat16, "attend: q")
-        lens = self._ints(seq_lens, self._lens_shape, "attend: seq_lens")
-        if out is None:
-            out = _empty(shape, torch.bfloat16, dev, stream)
-        if lse is None:
-            lse = _empty(self._lse_shape, torch.float32, dev, stream)
-        if workspace is None:
-            workspace = _empty(self._ws_bytes, torch.uint8, dev, stream)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            _refuse(f"attend: a contiguous workspace on {dev} is wanted")
-        check(mk_cache_attend(self.h, layer, qp, lens, prefix_len, scale,
-                              self._buffer(out, shape, torch.bfloat16, "attend: out"),
-                              self._buffer(lse, self._lse_shape, torch.float32, "attend: lse"), workspace.data_ptr(),
-                              workspace.nbytes, _raw_stream(self._index, stream)), "mk_cache_attend")
-        return out, lse
+        if stream is not None:
+            with self.torch.cuda.stream(stream):
+                return self._call.attend(self.h, layer, q, seq_lens, prefix_len, scale, out, lse, workspace)
+        return self._call.attend(self.h, layer, q, seq_lens, prefix_len, scale, out, lse, workspace)
 
     def status(self, stream=None):
         """First error recorded on the device since the last call (synchronises the stream)."""
-        return mk_cache_get_status(self.h, _raw_stream(self._index, stream))
+        return mk_cache_get_status(self.h, (stream or self.torch.cuda.current_stream(self.device)).cuda_stream)
 
     def close(self):
         if getattr(self, "h", None):
             mk_cache_destroy(self.h)
-            self.h = None
+            self.h = 0
 
     def __del__(self):
         try:
@@ -505,21 +436,12 @@ class Cache:
 def token_logprobs(logits, tokens, top_k=0, stream=None):
     """Scores of tokens (int32 [n]) under logits (bf16 or fp32 [n][vocab], rows any stride apart): (logprob fp32
     [n], entropy fp32 [n], ids int32 [n][top_k], their log probabilities fp32 [n][top_k]); see mk_token_logprobs."""
-    import torch
-    if not (logits.is_cuda and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)):
-        _refuse("token_logprobs: device logits [n][vocab] with contiguous rows are wanted")
-    code, dev, (n, V) = _float_dtype(logits, "token_logprobs"), logits.device, logits.shape
-    if not (tokens.dtype is torch.int32 and tokens.shape == (n,) and tokens.device == dev and tokens.is_contiguous()):
-        _refuse(f"token_logprobs: contiguous int32 tokens of shape ({n},) on {dev} are wanted")
-    if not 0 <= top_k <= 32:
-        _refuse("token_logprobs: top_k 0..32 is wanted")
-    logprob, entropy = _empty((2, n), torch.float32, dev, stream).unbind(0)
-    ids = _empty((n, top_k), torch.int32, dev, stream)
-    tops = _empty((n, top_k), torch.float32, dev, stream)
-    check(mk_token_logprobs(logits.data_ptr(), code, logits.stride(0), n, V, tokens.data_ptr(), logprob.data_ptr(),
-                            entropy.data_ptr(), top_k, ids.data_ptr(), tops.data_ptr(), dev.index,
-                            _raw_stream(dev.index, stream)), "mk_token_logprobs")
-    return logprob, entropy, ids, tops
+    call = _torch_calls or _calls()
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return call.token_logprobs(logits, tokens, top_k)
+    return call.token_logprobs(logits, tokens, top_k)
 
 
 def weight_structs(cfg, weights, k_cache, v_cache):

@@ -221,7 +221,7 @@ def test_caller_buffers_and_same_bits_every_time():
     c = handle(s)
     out = torch.empty_like(s["q"])
     lse = torch.empty((9, 16), device="cuda")
-    ws = torch.full((c._ws_bytes,), 0xFF, dtype=torch.uint8, device="cuda")    # NaN everywhere
+    ws = torch.full((c.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")    # NaN everywhere
     a = c.attend(1, s["q"], s["seq_lens"], prefix_len=400, out=out, lse=lse, workspace=ws)
     assert a[0] is out and a[1] is lse
     check(s, out, lse)
