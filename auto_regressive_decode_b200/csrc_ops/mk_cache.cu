@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <mutex>
 #include <new>
 
 #include "mk_cache.h"
@@ -50,15 +51,42 @@ cudaError_t encode_maps(const void* base, int64_t rows, int hd, int small_rows, 
 }
 
 // (cos, sin) of pos * theta^(-2i/hd), angles and functions in double: an angle
-// of a far position has no fraction left in fp32.
+// of a far position has no fraction left in fp32.  A thread keeps its i.
 __global__ void rope_table(float2* out, int T, int half, double theta) {
-  const int64_t n = (int64_t)T * half;
-  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
-    const int pos = (int)(e / half), i = (int)(e % half);
+  const int i = threadIdx.x % half, rows = blockDim.x / half;
+  const double freq = pow(theta, -(double)i / half);
+  for (int pos = blockIdx.x * rows + threadIdx.x / half; pos < T; pos += gridDim.x * rows) {
     double s, c;
-    sincos((double)pos * pow(theta, -(double)i / half), &s, &c);
-    out[e] = make_float2((float)c, (float)s);
+    sincos(pos * freq, &s, &c);
+    out[(int64_t)pos * half + i] = make_float2((float)c, (float)s);
   }
+}
+
+// Device memory of the handles, from a pool of the library that keeps what is
+// freed: cudaMalloc and cudaFree take milliseconds next to live work.
+cudaError_t pool_of(int dev, cudaMemPool_t* out) {
+  static std::mutex lock;
+  static cudaMemPool_t pools[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> hold(lock);
+  if (!pools[dev]) {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t p;
+    cudaError_t e = cudaMemPoolCreate(&p, &props);
+    if (e != cudaSuccess) return e;
+    uint64_t keep = UINT64_MAX;
+    e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) {
+      cudaMemPoolDestroy(p);
+      return e;
+    }
+    pools[dev] = p;
+  }
+  *out = pools[dev];
+  return cudaSuccess;
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -147,7 +175,9 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
     return e == cudaErrorInvalidValue ? MK_ERR_UNSUPPORTED : MK_ERR_CUDA;
   }
   const size_t table = sizeof(float2) * (size_t)d.max_ctx * (d.head_dim / 2);
-  if (cudaMalloc(&c->region, 256 + table) != cudaSuccess) {
+  cudaMemPool_t pool;
+  if (mk::pool_of(dev, &pool) != cudaSuccess ||
+      cudaMallocFromPoolAsync(&c->region, 256 + table, pool, cudaStreamPerThread) != cudaSuccess) {
     cudaGetLastError();
     delete c;
     return MK_ERR_CUDA;
@@ -167,12 +197,12 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
   }
   w.status = (int*)c->region;
   c->rope = (float2*)((uint8_t*)c->region + 256);
-  mk::rope_table<<<n_sm * 4, 256>>>(c->rope, d.max_ctx, d.head_dim / 2, (double)d.rope_theta);
+  mk::rope_table<<<n_sm * 4, 256, 0, cudaStreamPerThread>>>(c->rope, d.max_ctx, d.head_dim / 2, (double)d.rope_theta);
   // the table is ready when this returns: calls may come on any stream
-  if (cudaGetLastError() != cudaSuccess || cudaMemset(c->region, 0, 256) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
+  if (cudaGetLastError() != cudaSuccess || cudaMemsetAsync(c->region, 0, 256, cudaStreamPerThread) != cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamPerThread) != cudaSuccess) {
     cudaGetLastError();
-    cudaFree(c->region);
+    cudaFreeAsync(c->region, cudaStreamPerThread);
     delete c;
     return MK_ERR_CUDA;
   }
@@ -185,7 +215,9 @@ extern "C" int mk_cache_destroy(mk_cache* c) {
   cudaError_t e;
   {
     mk::OnDevice here(c->device);
-    e = cudaFree(c->region);
+    e = cudaDeviceSynchronize();  // calls on any stream may still read the table
+    const cudaError_t f = cudaFreeAsync(c->region, cudaStreamPerThread);
+    if (e == cudaSuccess) e = f;
   }
   delete c;
   return mk::launched(e);

@@ -124,6 +124,7 @@ struct Shared {
   uint32_t raised, hint;    // upper words of limits: from the groups' maxima, and the highest that a warp found by itself
   int held[kWarps];
   int n_best, dead;
+  float given;              // the given token's logit
   Sum part[kWarps];
   Sum sum;                  // this block's
 };
@@ -171,6 +172,13 @@ struct Part {
     }
   }
 };
+
+// The given token's logit; NaN for a token that is none.
+template <typename T>
+__device__ __forceinline__ float given_logit(const ScoreParams& p, const T* x, int row) {
+  const int t = __ldg(p.tokens + row);
+  return t >= 0 && t < p.vocab ? Vec<T>::one(x[t]) : NAN;
+}
 
 // A thread's sums.  d = x log2 e - c is one fma, c = m log2 e rounded; what the
 // rounding left (res) is put right when the sums move to another reference.
@@ -268,8 +276,9 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
           }
       }
     }
-    __syncwarp();
-    if (parts > 1) {
+    if (parts > 1) {  // one row, on which the compute warps have no time to wait for a word
+      if (lane == 0 && part == 0) sh.given = given_logit<T>(p, reinterpret_cast<const T*>(p.logits) + (int64_t)row0 * p.stride, row0);
+      __syncwarp();
       cluster.sync();
       cluster.sync();
     }
@@ -293,10 +302,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     };
     int held = 0;   // keys of this warp
     float given = NAN;
-    if (tid == 0 && part == 0) {
-      const int t = __ldg(p.tokens + row);
-      if (t >= 0 && t < p.vocab) given = Vec<T>::one(r.x[t]);
-    }
+    if (tid == 0 && parts == 1) given = given_logit<T>(p, r.x, row);
     if (tid == 0) sh.hint = 0;
     // the keys of a warp, a lane each (0: none), into its room; a full room is cut to its k best
     auto push = [&](Key key) {
@@ -469,16 +475,15 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
           a = warp_join(lane < parts ? cluster.map_shared_rank(&sh, lane)->sum : Sum{-INFINITY, 0.f, 0.f});
           if (lane == 0) sh.sum = a;
         }
-        // the blocks' best keys side by side
-        n = 0;
-        for (int i = 0; i < parts; ++i) {
-          const S* o = cluster.map_shared_rank(&sh, i);
-          const int m = o->n_best;
-          if (tid < m) sh.keys[n + tid] = o->best[tid];
-          n += m;
+        // the blocks' best keys side by side (0 where one has fewer), one remote read a thread
+        n = parts * k;
+        for (int i = tid; i < n; i += NT) {
+          const S* o = cluster.map_shared_rank(&sh, i / k);
+          sh.keys[i] = i % k < o->n_best ? o->best[i % k] : 0;
         }
+        got = lane < parts ? cluster.map_shared_rank(&sh, lane)->n_best : 0;
+        got = min(__reduce_add_sync(0xffffffffu, got), k);
         compute_bar<NT>();
-        got = min(n, k);
         rank_keys(sh.keys, n, k, sh.best, tid, NT);
         compute_bar<NT>();
       }
@@ -489,6 +494,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       const float lnz = logf(q.z);
       const bool none = !(q.z > 0.f) || isinf(q.m) || *dead;  // NaN, infinities, nothing allowed (or a copy that never came)
       if (tid == 0) {
+        if (parts > 1) given = sh.given;
         p.logprob[row] = none ? NAN : given - q.m - lnz;
         if (p.entropy) p.entropy[row] = none ? NAN : lnz - kLn2 * q.s / q.z;
       }
