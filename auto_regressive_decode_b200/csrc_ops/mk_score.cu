@@ -136,8 +136,21 @@ __device__ __forceinline__ void compute_bar() {
 }
 
 // Largest k of the n keys at `keys`, sorted, to `best` (not `keys` itself), by
-// comparison with all; threads t of nt (whole warps), n <= 2 nt.
+// comparison with all; threads t of nt (whole warps), n <= 2 nt.  Few keys: a key's
+// comparisons are shared by four threads.
 __device__ __forceinline__ void rank_keys(const Key* keys, int n, int k, Key* best, int t, int nt) {
+  if (n <= nt / 4) {
+    const int e = t / 4;
+    if ((t & ~31) / 4 >= n) return;
+    const Key a = e < n ? keys[e] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int i = t % 4; i < n; i += 4) rank += keys[i] > a;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (e < n && t % 4 == 0 && rank < k) best[rank] = a;
+    return;
+  }
   for (; (t & ~31) < n; t += nt) {
     const Key a = t < n ? keys[t] : 0;
     int rank = 0;
@@ -424,14 +437,22 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
           compute_bar<NT>();
           set_limit((Key)max(sh.raised, *(volatile uint32_t*)&sh.hint) << 32);
         }
-        // the warp looks through its candidates one by one, a lane a logit
+        // the warp looks through its candidates, a lane a logit: one at a time, or two whose 16 logits fill a half warp each
         uint32_t todo = __ballot_sync(0xffffffffu, top >= least);
         while (todo) {
-          const int t = (tid & ~31) + __ffs(todo) - 1, u = lane / VEC, i = lane % VEC, v = v0 + u * NT + t;
+          constexpr int kMine = U * VEC;  // logits of a thread
+          int t = __ffs(todo) - 1;
           todo &= todo - 1;
+          bool there = true;
+          if (kMine < 32 && lane >= kMine) {
+            t = __ffs(todo) - 1;
+            there = t >= 0;
+          }
+          if (kMine < 32) todo &= todo - 1;
+          const int at = lane % kMine, u = at / VEC, i = at % VEC, v = v0 + u * NT + (tid & ~31) + t;
           Key key = 0;
-          if (u < U && v < r.v1) {
-            const float f = Vec<T>::one(here[(u * NT + t) * VEC + i]);
+          if (there && v < r.v1) {
+            const float f = Vec<T>::one(here[(v - v0) * VEC + i]);
             if (f > -INFINITY) key = make_key(f, v * VEC - r.skew + i);
           }
           push(key);
