@@ -16,9 +16,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreadsA = 128;
-constexpr int kRowsInFlight = 4;  // rows a lane loads before it uses the first
-
 struct AppendParams {
   CacheView c;
   int layer, n_tokens;
@@ -58,11 +55,16 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Block (t, y): token t, rows y * slots + slot, stepping by all slots of the token.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreadsA) append_kernel(const __grid_constant__ AppendParams p) {
+// Block (t, y): token t, rows y * kSlots + slot, stepping by all slots of the
+// token.  kSlots rows at once, R of them in a lane's registers before it uses
+// the first.  A token's place takes three loads that wait for each other; what
+// hides them is the number of resident blocks, hence few threads and registers a
+// block: 16000 tokens of 32 rows of 64 took 43 us with 32 slots and R = 4, 25 us with 16 and 2.
+// Tokens of many rows want the larger block: 16384 of 120 fp32 rows of 128 245 us with 16 slots, 230 with 32.
+template <typename T, int HD, int kSlots, int R>
+__global__ void __launch_bounds__(kSlots * HD / 16) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = HD / 16;              // lanes of a row
-  constexpr int kSlots = kThreadsA / kLanes;   // rows a block holds at once
+  constexpr int kThreadsA = kSlots * kLanes;
   const CacheView& c = p.c;
   const int t = blockIdx.x, lane = threadIdx.x % kLanes, slot = blockIdx.y * kSlots + threadIdx.x / kLanes;
   const int step = gridDim.y * kSlots;
@@ -75,10 +77,10 @@ __global__ void __launch_bounds__(kThreadsA) append_kernel(const __grid_constant
     const int head = h < nq ? h : (h < nq + c.nkv ? h - nq : h - nq - c.nkv);
     return reinterpret_cast<const T*>(base) + (int64_t)head * HD + lane * 8;
   };
-  Vec8<T> x[kRowsInFlight][2];
+  Vec8<T> x[R][2];
   auto fetch = [&](int h0) {
 #pragma unroll
-    for (int r = 0; r < kRowsInFlight; ++r) {
+    for (int r = 0; r < R; ++r) {
       const int h = h0 + r * step;
       if (h < nh) {
         const T* s = source(h);
@@ -125,10 +127,10 @@ __global__ void __launch_bounds__(kThreadsA) append_kernel(const __grid_constant
   }
   // Whole warps walk the rows together (the norm's sums are warp shuffles).
   const int warp_slot = blockIdx.y * kSlots + (threadIdx.x & ~31) / kLanes;
-  for (int h0 = warp_slot, mine = slot; h0 < nh; h0 += kRowsInFlight * step, mine += kRowsInFlight * step) {
+  for (int h0 = warp_slot, mine = slot; h0 < nh; h0 += R * step, mine += R * step) {
     if (h0 != warp_slot) fetch(mine);
 #pragma unroll
-    for (int r = 0; r < kRowsInFlight; ++r) {
+    for (int r = 0; r < R; ++r) {
       const int h = mine + r * step;
       float lo[8], hi[8];
       if (h < nh) {
@@ -178,6 +180,17 @@ __global__ void __launch_bounds__(kThreadsA) append_kernel(const __grid_constant
   }
 }
 
+typedef void (*Kernel)(AppendParams);
+template <typename T, int HD, int kSlots>
+Kernel pick(int rows) {
+  return rows <= 1 ? append_kernel<T, HD, kSlots, 1>
+                   : (rows == 2 ? append_kernel<T, HD, kSlots, 2> : (rows == 3 ? append_kernel<T, HD, kSlots, 3> : append_kernel<T, HD, kSlots, 4>));
+}
+template <typename T, int HD>
+Kernel pick(int slots, int rows) {
+  return slots == 16 ? pick<T, HD, 16>(rows) : pick<T, HD, 32>(rows);
+}
+
 }  // namespace
 
 cudaError_t append(const mk_cache& c, int layer, const mk_append_args& a, cudaStream_t stream) {
@@ -185,18 +198,15 @@ cudaError_t append(const mk_cache& c, int layer, const mk_append_args& a, cudaSt
   AppendParams p{c.view, layer, a.n_tokens, a.q, a.k, a.v, a.q_stride * es, a.k_stride * es, a.v_stride * es,
                  a.starts, a.seq_lens, a.positions, (const uint16_t*)a.q_norm, (const uint16_t*)a.k_norm,
                  (uint16_t*)a.q_out, c.k, c.v, c.rope, c.d.rms_eps};
-  const int slots = kThreadsA / (c.d.head_dim / 16);
   const int nh = (a.q ? c.d.n_q_heads : 0) + 2 * c.d.n_kv_heads;
+  const int slots = nh <= 64 ? 16 : 32;  // four rows a lane, or more
   // Few tokens: their rows are spread over more blocks, until the SMs have two each.
   const int most = (nh + slots - 1) / slots, want = (2 * c.n_sm + a.n_tokens - 1) / a.n_tokens;
   const dim3 grid(a.n_tokens, want < most ? want : most);
-  if (c.d.head_dim == 128) {
-    if (es == 2) append_kernel<uint16_t, 128><<<grid, kThreadsA, 0, stream>>>(p);
-    else append_kernel<float, 128><<<grid, kThreadsA, 0, stream>>>(p);
-  } else {
-    if (es == 2) append_kernel<uint16_t, 64><<<grid, kThreadsA, 0, stream>>>(p);
-    else append_kernel<float, 64><<<grid, kThreadsA, 0, stream>>>(p);
-  }
+  const int rows = (most + (int)grid.y - 1) / (int)grid.y;  // a lane's
+  const auto kernel = c.d.head_dim == 128 ? (es == 2 ? pick<uint16_t, 128>(slots, rows) : pick<float, 128>(slots, rows))
+                                          : (es == 2 ? pick<uint16_t, 64>(slots, rows) : pick<float, 64>(slots, rows));
+  kernel<<<grid, slots * (c.d.head_dim / 16), 0, stream>>>(p);
   return cudaGetLastError();
 }
 
