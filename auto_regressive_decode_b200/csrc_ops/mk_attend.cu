@@ -38,7 +38,10 @@ constexpr int kComputeThreads = kWarps * 32;
 constexpr int kAttThreads = kComputeThreads + 32;
 constexpr int kHead = 2;                         // tiles that a group's start and end count as
 constexpr int kMaxRows = 64;                     // rows of a prefix row tile
-constexpr int kTcFrom = 16;                      // more rows of a KV head than this share a prefix: tensor-core kernel
+// Rows of a KV head that share a prefix: more go to the tensor-core kernel, which does 128 in the time of one.
+// 32 rows over 2500 positions (8 KV heads) take 16.5 us here and 18.4 there, 64 rows 21.0 and 20.3; over 16000 27.5 and
+// 26.4, 39.9 and 28.3.
+constexpr int kTcFrom = 32;
 
 template <int HD, bool NARROW>
 struct Layout {
@@ -187,6 +190,15 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
     ctl->dead = 0;
     fence_mbar_init();
   }
+  if (tid == kComputeThreads) {
+    prefetch_map(&kwhole);
+    prefetch_map(&vwhole);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  // Nothing is read or written before the kernel ahead is done (after attend_prefix_tc: the one ahead of
+  // that, whose own wait precedes this launch; their workspaces are apart).
+  if (!p.tc) grid_wait();
   grid_launch_next();
   for (int b = tid; b < c.B; b += kAttThreads) {
     const int n = __ldg(p.seq_lens + b), m = n < 0 ? 0 : min(n, c.T);
@@ -684,7 +696,7 @@ cudaError_t run(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   // blocks of the next kernel are set up while this one's are still under way
-  cfg.numAttrs = p.tc;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kAttThreads);
   cfg.dynamicSmemBytes = smem;

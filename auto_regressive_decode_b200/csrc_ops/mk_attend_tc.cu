@@ -134,7 +134,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fence_mbar_init();
   }
   if (warp == 16) tmem_alloc(smem_addr(&ctl->tmem), 512);
+  if (tid == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   __syncthreads();
+  grid_wait();  // nothing is read or written before the kernel ahead is done
   grid_launch_next();
   int longest = 0;
   for (int b = tid; b < cv.B; b += kTcThreads) longest = max(longest, min(__ldg(p.seq_lens + b), cv.T));
@@ -437,11 +442,21 @@ cudaError_t attend_prefix_tc_prepare() {
 }
 
 cudaError_t attend_prefix_tc(const AttendParams& p, const mk_cache& c, cudaStream_t stream) {
-  if (c.d.head_dim == 128)
-    attend_prefix_kernel<128><<<c.n_sm, kTcThreads, TcLayout<128>::kTotal, stream>>>(p, c.ktall, c.vtall, c.tall);
-  else
-    attend_prefix_kernel<64><<<c.n_sm, kTcThreads, TcLayout<64>::kTotal, stream>>>(p, c.ktall, c.vtall, c.tall);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the kernel ahead is under way
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(c.n_sm);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.stream = stream;
+  if (c.d.head_dim == 128) {
+    cfg.dynamicSmemBytes = TcLayout<128>::kTotal;
+    return cudaLaunchKernelEx(&cfg, attend_prefix_kernel<128>, p, c.ktall, c.vtall, c.tall);
+  }
+  cfg.dynamicSmemBytes = TcLayout<64>::kTotal;
+  return cudaLaunchKernelEx(&cfg, attend_prefix_kernel<64>, p, c.ktall, c.vtall, c.tall);
 }
 
 }  // namespace mk
