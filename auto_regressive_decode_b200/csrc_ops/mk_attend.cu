@@ -248,48 +248,50 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
     const int boxes = kTile / p.box;               // boxes of one 64-column block of a tile that is no single box
     const int cb = lane / boxes, j = lane % boxes; // this lane's box
     const bool boxed = cb < HD / 64;
-    int lo = 0, hi = 0, start = 0, i = 0, row = 0;
-    bool one = false, wanted = false;
-    // This lane's box of tile i of the piece.
-    auto place = [&]() {
-      const int t0 = start + i * kTile;
-      one = p.whole && t0 >= lo && t0 + kTile <= hi;
-      const int at = one ? t0 : t0 + j * p.box;
-      wanted = one ? lane == 0 : boxed && at < hi && at + p.box > lo;
-      bool ok = true;
-      if (wanted) row = (int)(c.row(p.layer, a.b, at, &ok) + a.kvh * c.head_pitch());
-      if (!ok) set_status(c.status, MK_ERR_RANGE, a.b);
-    };
-    auto open = [&]() {  // the next piece
-      if (!walk.next(a)) return false;
-      start = a.shared ? 0 : p.base;
-      lo = a.shared ? 0 : p.prefix;
-      hi = a.shared ? prefix_end : lens[a.b];
-      i = a.i0;
-      place();
-      // its query rows
-      const int rows = piece_rows(p, a);
-      const uint32_t full = smem_addr(&ctl->qfull[qbuf]), dst = ring + S::kQ + qbuf * S::kQRows * S::kQPitch;
-      mbar_wait(smem_addr(&ctl->qempty[qbuf]), qphase ^ 1, dead);
-      if (!__any_sync(0xffffffffu, *dead)) {
-        if (lane == 0) mbar_expect_tx(full, rows * HD * 2);
-        __syncwarp();
-        for (int r = lane; r < rows; r += 32) {
-          const int b = a.shared ? (a.tile0 + r) / p.group : a.b, jh = a.shared ? (a.tile0 + r) % p.group : r;
-          bulk_load(dst + r * S::kQPitch, p.q + ((int64_t)b * c.nq + a.kvh * p.group + jh) * HD, HD * 2, full);
+    int lo = 0, hi = 0, start = 0, i = 0;
+    // Tiles in order; the place of the next one is looked up while this one's copies are under way.
+    int i1 = 0;  // end of the open piece
+    bool have = false, one_now = false, wanted_now = false;
+    int row_now = 0;
+    uint32_t bytes = 0;
+    while (true) {
+      bool more = true;
+      if (i == i1) {  // the next piece: its tiles, its query rows
+        more = walk.next(a);
+        if (more) {
+          i = a.i0;
+          i1 = a.i1;
+          start = a.shared ? 0 : p.base;
+          lo = a.shared ? 0 : p.prefix;
+          hi = a.shared ? prefix_end : lens[a.b];
+          const int rows = piece_rows(p, a);
+          const uint32_t full = smem_addr(&ctl->qfull[qbuf]), dst = ring + S::kQ + qbuf * S::kQRows * S::kQPitch;
+          mbar_wait(smem_addr(&ctl->qempty[qbuf]), qphase ^ 1, dead);
+          if (!__any_sync(0xffffffffu, *dead)) {
+            if (lane == 0) mbar_expect_tx(full, rows * HD * 2);
+            __syncwarp();
+            for (int r = lane; r < rows; r += 32) {
+              const int b = a.shared ? (a.tile0 + r) / p.group : a.b, jh = a.shared ? (a.tile0 + r) % p.group : r;
+              bulk_load(dst + r * S::kQPitch, p.q + ((int64_t)b * c.nq + a.kvh * p.group + jh) * HD, HD * 2, full);
+            }
+          }
+          if (p.wide || qbuf) qphase ^= 1;
+          qbuf = p.wide ? 0 : qbuf ^ 1;
         }
       }
-      if (p.wide || qbuf) qphase ^= 1;
-      qbuf = p.wide ? 0 : qbuf ^ 1;
-      return true;
-    };
-    bool more = open();
-    while (more) {
-      const bool one_now = one, wanted_now = wanted;
-      const int row_now = row;
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, wanted_now));
-      const uint32_t bytes = one_now ? S::kSlotBytes : n * p.box * 128;
-      for (int kv = 0; kv < 2; ++kv) {
+      bool one = false, wanted = false;
+      int row = 0;
+      if (more) {  // this lane's box of tile i
+        const int t0 = start + i * kTile;
+        one = p.whole && t0 >= lo && t0 + kTile <= hi;
+        const int at = one ? t0 : t0 + j * p.box;
+        wanted = one ? lane == 0 : boxed && at < hi && at + p.box > lo;
+        bool ok = true;
+        if (wanted) row = (int)(c.row(p.layer, a.b, at, &ok) + a.kvh * c.head_pitch());
+        if (!ok) set_status(c.status, MK_ERR_RANGE, a.b);
+        ++i;
+      }
+      for (int kv = 0; kv < 2 && have; ++kv) {  // the tile looked up before
         const uint32_t full = smem_addr(&ctl->full[slot]), dst = ring + slot * S::kSlotBytes;
         mbar_wait(smem_addr(&ctl->empty[slot]), phase ^ 1, dead);
         if (!__any_sync(0xffffffffu, *dead)) {
@@ -302,11 +304,13 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
         }
         __syncwarp();
         if (++slot == S::kSlots) slot = 0, phase ^= 1;
-        if (kv == 0) {  // the next tile's place is looked up while this one's copies are under way
-          if (++i < a.i1) place();
-        }
       }
-      if (i >= a.i1) more = open();
+      if (!more) break;
+      have = true;
+      one_now = one;
+      wanted_now = wanted;
+      row_now = row;
+      bytes = one ? S::kSlotBytes : __popc(__ballot_sync(0xffffffffu, wanted)) * p.box * 128;
     }
     // a block that gave up waits for its own copies in flight before it ends
     if (__any_sync(0xffffffffu, *dead)) {
@@ -580,11 +584,16 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   const int n0 = (r0.y - r0.x + 1) * (both ? 2 : 1), n = n0 + r1.y - r1.x + 1, step = both ? entry : per;
   const int64_t at0 = (int64_t)(r0.x + g0) * per + (both ? row % entry : row % per), at1 = (int64_t)(r1.x + g1) * p.group + j;
 
+  // piece i of the row: its (m, l), and its output from this lane's columns on
+  const float2* ml0 = p.pre_ml + at0;
+  const float2* ml1 = p.own_ml + (at1 - (int64_t)n0 * p.group);
+  const float* o0 = p.pre_o + at0 * HD + lane * V;
+  const float* o1 = p.own_o + (at1 - (int64_t)n0 * p.group) * HD + lane * V;
   float M = -INFINITY, L = 0.f, o[V] = {};
   for (int i0 = sub; i0 < n; i0 += 32 * W) {  // 32 pieces at a time: a lane's weight, then the weighted sum
     const int i = i0 + lane * W;
     float2 x = make_float2(-INFINITY, 0.f);
-    if (i < n) x = i < n0 ? p.pre_ml[at0 + (int64_t)i * step] : p.own_ml[at1 + (int64_t)(i - n0) * p.group];
+    if (i < n) x = i < n0 ? ml0[(int64_t)i * step] : ml1[(int64_t)i * p.group];
     float m = x.x;
 #pragma unroll
     for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
@@ -599,13 +608,13 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] *= back;
     const int k = min(32, (n - i0 + W - 1) / W);
-#pragma unroll 8
+#pragma unroll 4
     for (int q = 0; q < k; ++q) {
       const int iq = i0 + q * W;
-      const float* po = iq < n0 ? p.pre_o + (at0 + (int64_t)iq * step) * HD : p.own_o + (at1 + (int64_t)(iq - n0) * p.group) * HD;
+      const float* po = iq < n0 ? o0 + (int64_t)iq * (step * HD) : o1 + (int64_t)iq * (p.group * HD);
       float v[V];
-      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po + lane * 4);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po + lane * 2);
+      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po);
       const float wq = __shfl_sync(0xffffffffu, w, q);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = wq == 0.f ? o[e] : fmaf(v[e], wq, o[e]);

@@ -10,9 +10,9 @@
 //   warps 0-7, 8-15 softmax of stream 0, 1, two threads a row (half the columns
 //                   each): S from tensor memory, maximum and sum of the row, P =
 //                   2^(s - m) as bf16 over S's columns
-//   warp 16         one thread issues the products
+//   warps 16, 18    one thread each issues the products of stream 0, 1, in turns
 //   warp 17         TMA of K and V tiles into a ring
-//   warps 18, 19    nothing: they fill the warpgroup that gives its registers to the softmax
+//   warp 19         nothing: it fills the warpgroup that gives its registers to the softmax
 //
 // A row's reference m is raised, and its output scaled, only when a score
 // exceeds it by kSlack (log2): p stays below 2^kSlack, far inside fp32 and
@@ -214,72 +214,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       if (lane == 0) set_status(cv.status, MK_ERR_DEVICE_TIMEOUT, cta);
     }
-  } else if (warp == 16) {  // ---- products
+  } else if (warp == 16 || warp == 18) {  // ---- products of stream s
+    const int s = (warp - 16) / 2;
     constexpr uint32_t kQk = mma_desc(kTcRows, kTcTile, false), kPv = mma_desc(kTcRows, HD, true);
     const uint32_t leader = lane == 0;
     const uint64_t q_desc = smem_desc(base + S::kQ, 16, 1024), k_desc = smem_desc(base, 16, 1024),
                    v_desc = smem_desc(base, kTcTile * 128, 1024);
     uint32_t at = 0;  // tiles that passed through the ring in earlier pieces
-    uint32_t q_phase = 0, tail_phase = 0, p_phase0 = 0, p_phase1 = 0;
+    uint32_t q_phase = 0, tail_phase = 0, p_phase = 0;
+    const uint32_t s_full = smem_addr(&ctl->s_full[s]), p_full = smem_addr(&ctl->p_full[s]), o_done = smem_addr(&ctl->o_done[s]);
+    const uint32_t s_col = tmem + kS + s * 128, o_col = tmem + kO + s * 128;
+    // The streams' warps take turns.  A product is issued as the matrix unit takes it (65 to
+    // 71 clocks each, a commit 40 to 75), so that whatever stands between two runs of them is
+    // time lost: one warp waits for its operands while the other issues.
+    auto take_turn = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(9 + s) : "memory"); };
+    auto pass_turn = [&]() { asm volatile("bar.arrive %0, 64;" ::"r"(10 - s) : "memory"); };
+    if (s == 1) pass_turn();
     while (walk.next(a)) {
+      const int turns = a.pair ? a.n : (a.n + 1) / 2, n = a.pair ? a.n : (a.n + 1 - s) / 2;
+      const uint64_t q = q_desc + (a.pair ? s : 0) * (S::kQBytes >> 4);
       mbar_wait(smem_addr(&ctl->q_full), q_phase, dead);
       q_phase ^= 1;
-      // The products of a piece.  What stands between two runs of them is kept short: a
-      // product is issued as the matrix unit takes it (65 to 71 clocks each), and the unit
-      // idles meanwhile; a commit costs it 40 to 75.  So one commit a stream and tile tells
-      // the softmax that its scores are there, that the product before is done (in order of
-      // issue) and, through the softmax, the ring that the tiles have been read.
-      auto products = [&](auto pair_) {
-        constexpr bool kPair = decltype(pair_)::value;
-        const int n0 = kPair ? a.n : (a.n + 1) / 2, n1 = kPair ? a.n : a.n / 2;
-        auto qk = [&](auto s_, int i) {  // scores of the stream's tile i
-          constexpr int s = decltype(s_)::value;
-          const uint32_t place = at + k_place(kPair, kPair ? i : 2 * i + s), slot = place % S::kSlots;
-          if (!kPair || s == 0) mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
-          const uint64_t q = q_desc + (kPair ? s : 0) * (S::kQBytes >> 4), k = k_desc + slot * (S::kSlotBytes >> 4);
+      auto k_tile = [&](int i) {  // the descriptor of the stream's K tile i, once it is there
+        const uint32_t place = at + k_place(a.pair, a.pair ? i : 2 * i + s), slot = place % S::kSlots;
+        mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
+        return k_desc + slot * (S::kSlotBytes >> 4);
+      };
+      auto qk = [&](uint64_t k) {  // scores
 #pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks) {  // 16 columns are 32 bytes of a swizzled line; 4 k-steps a 64-column block
-            constexpr uint32_t kBlock = kTcRows * 128 >> 4;
-            const uint32_t off = ks / 4 * kBlock + ks % 4 * 2;
-            tc_mma_ss(tmem + kS + s * 128, q + off, k + off, kQk, ks > 0, leader);
-          }
-          tc_commit(smem_addr(&ctl->s_full[s]), leader);
-        };
-        auto pv = [&](auto s_, int i, int n, uint32_t& p_phase) {
-          constexpr int s = decltype(s_)::value;
-          const int t = kPair ? i : 2 * i + s;
-          const uint32_t place = at + v_place(kPair, t, a.n), slot = place % S::kSlots;
-          if (!kPair || s == 0) {
-            mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
-            if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail), tail_phase, dead);
-          }
-          const uint64_t v = v_desc + slot * (S::kSlotBytes >> 4);
-          constexpr uint32_t kD = kO + s * 128, kP = kS + s * 128;
-          mbar_wait(smem_addr(&ctl->p_full[s]), p_phase, dead);
+        for (int ks = 0; ks < HD / 16; ++ks) {  // 16 columns are 32 bytes of a swizzled line; 4 k-steps a 64-column block
+          constexpr uint32_t kBlock = kTcRows * 128 >> 4;
+          const uint32_t off = ks / 4 * kBlock + ks % 4 * 2;
+          tc_mma_ss(s_col, q + off, k + off, kQk, ks > 0, leader);
+        }
+        // tells the softmax that the scores are there, that the product before is done (in order of
+        // issue) and, through the softmax, the ring that both tiles have been read
+        tc_commit(s_full, leader);
+      };
+      uint64_t k = n ? k_tile(0) : 0;
+      take_turn();
+      if (n) qk(k);
+      pass_turn();
+      for (int i = 0; i < turns; ++i) {
+        uint64_t v = 0;
+        if (i < n) {
+          const int t = a.pair ? i : 2 * i + s;
+          const uint32_t place = at + v_place(a.pair, t, a.n), slot = place % S::kSlots;
+          mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
+          if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail), tail_phase, dead);
+          v = v_desc + slot * (S::kSlotBytes >> 4);
+          if (i + 1 < n) k = k_tile(i + 1);
+          mbar_wait(p_full, p_phase, dead);
           p_phase ^= 1;
-          tc_fence_after();
+        }
+        take_turn();
+        tc_fence_after();
+        if (i < n) {
 #pragma unroll
           for (int ks = 0; ks < kTcTile / 16; ++ks)  // 16 lines on
-            tc_mma_ts(tmem + kD, tmem + kP + ks * 8, v + ks * (16 * 128 >> 4), kPv, ks > 0 || i > 0, leader);
-          if (i + 1 == n) tc_commit(smem_addr(&ctl->o_done[s]), leader);
-        };
-        const std::integral_constant<int, 0> s0;
-        const std::integral_constant<int, 1> s1;
-        // A stream's next scores overwrite its probabilities: after the product that reads them, in order of issue.
-        qk(s0, 0);
-        if (n1) qk(s1, 0);
-        for (int i = 0; i < n0; ++i) {
-          pv(s0, i, n0, p_phase0);
-          if (i + 1 < n0) qk(s0, i + 1);
-          if (i < n1) pv(s1, i, n1, p_phase1);
-          if (i + 1 < n1) qk(s1, i + 1);
+            tc_mma_ts(o_col, s_col + ks * 8, v + ks * (16 * 128 >> 4), kPv, ks > 0 || i > 0, leader);
+          // The next scores overwrite the probabilities: after the product that reads them, in order of issue.
+          if (i + 1 < n) qk(k);
+          else tc_commit(o_done, leader);
         }
-      };
-      if (a.pair) products(std::true_type());
-      else products(std::false_type());
+        pass_turn();
+      }
       if (a.t0 + a.n > whole_tiles) tail_phase ^= 1;
       at += 2 * a.n;
     }
+    if (s == 0) take_turn();  // the last one passed
   }
   } else {  // ---- softmax of stream s
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));

@@ -42,28 +42,23 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 
-// Longest in-kernel wait (ns).  A wait that runs out marks the block dead
-// (`*dead`, shared memory): every later wait of the block returns at once, so
-// that all warps reach the end of the kernel in their usual order.
-constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead) {
-  uint64_t t0 = 0;
+// A wait is bounded by its tries (2^22, of 20 clocks and more each): it then
+// marks the block dead (`*dead`, shared memory), and every later wait of the
+// block returns soon, so that all warps reach the end of the kernel in their
+// usual order.  Counted, not timed: reading the timer woke waits up late, and its code in every wait was
+// slow to fetch where a kernel runs for microseconds.
+constexpr uint32_t kWaitTries = 1u << 22;
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
-    if (i & 255) continue;  // the timer is slow to read: a wait that looked at it every time woke up late
+    if (i & 255) continue;
     if (*dead) return false;
-    const uint64_t t = globaltimer();
-    if (!t0) t0 = t;
-    if (t - t0 > kWaitNs) {
+    if (i >= kWaitTries) {
       *dead = 1;
       return false;
     }
   }
   return true;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, dead);
 }
 
 // ---- TMA ---------------------------------------------------------------------------
