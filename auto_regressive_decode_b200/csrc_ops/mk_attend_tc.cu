@@ -292,8 +292,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float scale = fabsf(p.scale);
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the query's signs
     float* swap = reinterpret_cast<float*>(smem + S::kSwap) + s * 512;  // [turn][half][row]
+    auto stream_bar = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(11 + s) : "memory"); };
     auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + s * 4 + warp % 4) : "memory"); };
-    uint32_t q_phase = 0, s_phase = 0, o_phase = 0, at = 0, turn = 0;
+    uint32_t q_phase = 0, s_phase = 0, o_phase = 0, other_phase = 0, at = 0, turn = 0;
     // The other half's value for this row.
     auto other = [&](float mine) {
       float* w = swap + turn * 256;
@@ -413,18 +414,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         if (r == 0 && c == 0)
           mbar_arrive(smem_addr(&ctl->empty[(at + v_place(a.pair, a.pair ? n - 1 : 2 * n - 2 + s, a.n)) % S::kSlots]), a.pair ? 1 : 2);
-        float* out = p.pre_o + (entry * kTcRows + r) * HD + c * (HD / 2);
+        // The rows' outputs pass through the query tile's memory, which is free once the
+        // stream's products are done (with one row tile, once the other stream's are too): from a
+        // thread's row to whole lines of the workspace (32 lanes' 16 bytes of 32
+        // rows took a clock a lane, 7000 clocks a piece).
+        if (s == 0 && !a.pair && a.n > 1) mbar_wait(smem_addr(&ctl->o_done[1]), other_phase, dead);
+        float4* stage = reinterpret_cast<float4*>(smem + S::kQ + s * S::kQBytes);
+        constexpr int kChunks = HD / 8;      // 16-byte chunks of a row in a round: half its columns
+        constexpr int kMine = kChunks / 2;   // a thread's
+        float* out = p.pre_o + entry * kTcRows * HD;
 #pragma unroll 1
-        for (int q = 0; q < HD / 32; ++q) {
-          uint32_t y[16];
-          tmem_ld16(o_at + q * 16, y);
+        for (int round = 0; round < 2; ++round) {
+          uint32_t y[4 * kMine];
+          if constexpr (HD == 128) tmem_ld32(o_at + round * 32, y);
+          else tmem_ld16(o_at + round * 16, y);
           tmem_wait_ld();
-          if (valid) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + q * 16 + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          for (int e = 0; e < kMine; ++e)
+            stage[r * kChunks + ((c * kMine + e) ^ (r & 7))] =
+                make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+          stream_bar();
+#pragma unroll 4
+          for (int e = tid % 256; e < kTcRows * kChunks; e += 256) {
+            const int to = e / kChunks, ch = e % kChunks, half = ch / kMine;
+            if ((a.pair ? s * kTcRows : 0) + to < a.rows)
+              *reinterpret_cast<float4*>(out + to * HD + half * (HD / 2) + round * (HD / 4) + (ch % kMine) * 4) = stage[to * kChunks + (ch ^ (to & 7))];
           }
+          stream_bar();
         }
       }
+      if (a.pair || a.n > 1) other_phase ^= 1;  // stream 1 had products in this piece
       at += 2 * a.n;
     }
   }
