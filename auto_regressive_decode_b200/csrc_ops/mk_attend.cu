@@ -5,7 +5,7 @@
 // KV head, the prefix serves batch x group rows at once (group = query heads
 // per KV head), a sequence's own positions serve its group rows.  Both are cut
 // into tiles of kTile positions; a "group" is the tiles of one set of rows
-// (prefix: KV head x row tile; own: sequence x KV head).  The tiles of all
+// (prefix: KV head; own: sequence x KV head).  The tiles of all
 // groups, in order, are dealt to the blocks as equal contiguous runs (a group
 // counts kHead tiles more: what starting and ending it costs); a block's run
 // within a group is a piece, which keeps the running maximum m and sum l of
@@ -37,7 +37,6 @@ constexpr int kWarps = 4;                        // compute warps; the next one 
 constexpr int kComputeThreads = kWarps * 32;
 constexpr int kAttThreads = kComputeThreads + 32;
 constexpr int kHead = 2;                         // tiles that a group's start and end count as
-constexpr int kMaxRows = 64;                     // rows of a prefix row tile
 // Rows of a KV head that share a prefix: more go to the tensor-core kernel, which does 128 in the time of one.
 // 32 rows over 2500 positions (8 KV heads) take 16.5 us here and 18.4 there, 64 rows 21.0 and 20.3; over 16000 27.5 and
 // 26.4, 39.9 and 28.3.
@@ -77,7 +76,7 @@ __device__ __forceinline__ void compute_bar() { asm volatile("bar.sync 1, %0;" :
 // A piece: tiles [i0, i1) of a group.
 struct Piece {
   bool shared;
-  int b, kvh, tile0;  // own: the sequence; shared: first row of the row tile
+  int b, kvh;         // the sequence (shared: 0)
   int i0, i1, gidx;
   bool last;          // it ends its group
 };
@@ -92,13 +91,13 @@ struct Walk {
   int g, kvh, b, n, r;  // the group: prefix group or sequence and KV head; its cost, the run's place in it
   __device__ Walk(const AttendParams& prm, const int* cumulative, int pre, int u0, int u1)
       : p(prm), cum(cumulative), pre_tiles(pre), u(u0), end(u1) {
-    const int pre_cost = pre ? pre + kHead : 0, groups = p.c.nkv * p.row_tiles, shared_cost = groups * pre_cost;
+    const int pre_cost = pre ? pre + kHead : 0, shared_cost = p.c.nkv * pre_cost;
     shared = u < shared_cost;
     if (shared) {
       g = u / pre_cost;
       r = u - g * pre_cost;
       n = pre_cost;
-      kvh = g / p.row_tiles;
+      kvh = g;
       b = 0;
     } else {
       const int v = u - shared_cost, w = v / p.c.nkv;
@@ -120,18 +119,15 @@ struct Walk {
       if (r == n) {  // the next group
         r = 0;
         ++g;
-        if (shared) {
-          if (g < p.c.nkv * p.row_tiles) {
-            kvh = g / p.row_tiles;
-          } else {
-            shared = false;
-            g = kvh = 0;
-            b = 0;
-            n = cum[1];
-          }
-        } else if (++kvh == p.c.nkv) {
+        if (++kvh == p.c.nkv) {
           kvh = 0;
-          ++b;
+          if (shared) {
+            shared = false;
+            g = 0;
+            n = cum[1];
+          } else {
+            ++b;
+          }
         }
         while (!shared && (n = cum[b + 1] - cum[b]) == 0) {  // sequences without tiles; u < end: one follows
           ++b;
@@ -143,7 +139,6 @@ struct Walk {
       a.gidx = g;
       a.kvh = kvh;
       a.b = b;
-      a.tile0 = shared ? g % p.row_tiles * p.row_tile : 0;
       a.i0 = max(r - kHead, 0);
       a.i1 = r + take - kHead;
       u += take;
@@ -156,7 +151,7 @@ struct Walk {
 };
 
 __device__ __forceinline__ int piece_rows(const AttendParams& p, const Piece& a) {
-  return a.shared ? min(p.row_tile, p.c.B * p.group - a.tile0) : p.group;
+  return a.shared ? p.rows : p.group;
 }
 
 template <int HD, bool NARROW>
@@ -230,7 +225,7 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int pre_tiles = p.tc ? 0 : (prefix_end + kTile - 1) / kTile;
-  const int cost = (pre_tiles ? (pre_tiles + kHead) * p.row_tiles * c.nkv : 0) + cum[c.B] * c.nkv;
+  const int cost = (pre_tiles ? (pre_tiles + kHead) * c.nkv : 0) + cum[c.B] * c.nkv;
   if (blockIdx.x == 0) {
     for (int b = tid; b < c.B; b += kAttThreads) p.sched[1 + b] = cum[b + 1] - cum[b];
     if (tid == 0) p.sched[0] = prefix_end;
@@ -271,7 +266,7 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
             if (lane == 0) mbar_expect_tx(full, rows * HD * 2);
             __syncwarp();
             for (int r = lane; r < rows; r += 32) {
-              const int b = a.shared ? (a.tile0 + r) / p.group : a.b, jh = a.shared ? (a.tile0 + r) % p.group : r;
+              const int b = a.shared ? r / p.group : a.b, jh = a.shared ? r % p.group : r;
               bulk_load(dst + r * S::kQPitch, p.q + ((int64_t)b * c.nq + a.kvh * p.group + jh) * HD, HD * 2, full);
             }
           }
@@ -345,7 +340,7 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = h ? row1 : row0;
-      lim[h] = r >= rows ? 0 : (a.shared ? min(lens[(a.tile0 + r) / p.group], hi) : hi);
+      lim[h] = r >= rows ? 0 : (a.shared ? min(lens[r / p.group], hi) : hi);
     }
     constexpr int kQRegs = NARROW ? 2 : 4;
     uint32_t qf[KS][kQRegs];
@@ -503,9 +498,8 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
       if ((NARROW ? gq : cq) == 0) sml[warp * 16 + (h ? row1 : row0) % 16] = make_float2(m[h], l[h]);
     }
     const int64_t pid = (int64_t)cta + a.gidx;
-    const int stride = a.shared ? p.row_tile : p.group;
-    float* po = (a.shared ? p.pre_o : p.own_o) + pid * stride * HD;
-    float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * stride;
+    float* po = (a.shared ? p.pre_o : p.own_o) + pid * rows * HD;
+    float2* pml = (a.shared ? p.pre_ml : p.own_ml) + pid * rows;
     if (tid == 0) {
       int2* at = (a.shared ? p.pre_blocks : p.own_blocks) + a.gidx;
       if (a.i0 == 0) at->x = cta;
@@ -533,18 +527,28 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
       compute_bar();
       constexpr int kQuads = S::kCols / 4;
       for (int e = tid; e < rows * kQuads; e += kComputeThreads) {
-        const int r = e / kQuads, col = e % kQuads * 4;
+        const int r = e / kQuads, col = e % kQuads * 4, w0 = NARROW ? 0 : r / 16;
         float M = -INFINITY, L = 0.f;
-        for (int w = r / 16; w < kWarps; w += R) M = fmaxf(M, sml[w * 16 + r % 16].x);
-        const float to = M == -INFINITY ? 0.f : M;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = r / 16; w < kWarps; w += R) {
-          const float2 ml = sml[w * 16 + r % 16];
+        auto ml_of = [&](int w) { return sml[w * 16 + r % 16]; };
+        auto add = [&](int w, float to) {
+          const float2 ml = ml_of(w);
           const float4 x = *reinterpret_cast<const float4*>(red + (w * S::kRedRows + r % 16) * S::kRedPitch + col);
-          if (ml.y == 0.f) continue;  // every position masked (a NaN sum is passed on)
+          if (ml.y == 0.f) return;  // every position masked (a NaN sum is passed on)
           const float f = ex2(ml.x - to);
           L += f * ml.y;
           sum.x += f * x.x; sum.y += f * x.y; sum.z += f * x.z; sum.w += f * x.w;
+        };
+        if constexpr (NARROW) {  // every warp has the row
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_of(w).x);
+          const float to = M == -INFINITY ? 0.f : M;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) add(w, to);
+        } else {
+          for (int w = w0; w < kWarps; w += R) M = fmaxf(M, ml_of(w).x);
+          const float to = M == -INFINITY ? 0.f : M;
+          for (int w = w0; w < kWarps; w += R) add(w, to);
         }
         *reinterpret_cast<float4*>(po + (int64_t)r * HD + part * S::kCols + col) = sum;
         if (part == 0 && col == 0) pml[r] = make_float2(M, L);
@@ -570,9 +574,9 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   const int row = b * p.group + j, g1 = b * c.nkv + kvh;
   // the prefix's pieces are entries of some rows: one a piece, or of kTcRows rows, two a piece: for
   // two row tiles, or, with one row tile in the group, for its even and odd tiles
-  const int entry = p.tc ? kTcRows : p.row_tile, per = p.tc ? 2 * kTcRows : entry;
-  const int g0 = p.tc ? kvh * p.tc_groups + row / per : kvh * p.row_tiles + row / per;
-  const bool both = p.tc && c.B * p.group - row / per * per <= kTcRows;
+  const int entry = p.tc ? kTcRows : p.rows, per = p.tc ? 2 * kTcRows : entry;
+  const int g0 = p.tc ? kvh * p.tc_groups + row / per : kvh;
+  const bool both = p.tc && p.rows - row / per * per <= kTcRows;
   grid_wait();
   const bool have = b < c.B;
   // the row's pieces: blocks [x, y] of its prefix group and of its own
@@ -661,24 +665,22 @@ struct Carve {
   }
 };
 struct Plan {
-  int row_tile, row_tiles, tc_groups;
+  int tc_groups;
   size_t sched, pre_blocks, own_blocks, pre_o, pre_ml, own_o, own_ml, total;
 };
 
 Plan plan(const mk_cache_desc& d, int n_sm) {
   Plan w;
   const int group = d.n_q_heads / d.n_kv_heads, rows = d.batch * group;
-  w.row_tile = std::min((rows + 15) / 16 * 16, kMaxRows);
-  w.row_tiles = (rows + w.row_tile - 1) / w.row_tile;
   // a piece more than its predecessor starts a block or a group: at most blocks + groups of them
   const size_t blocks = (size_t)n_sm * 3;
   w.tc_groups = (rows + 2 * kTcRows - 1) / (2 * kTcRows);
   const size_t pre = rows > kTcFrom ? ((size_t)n_sm + (size_t)d.n_kv_heads * w.tc_groups) * 2 * kTcRows
-                                    : (blocks + (size_t)d.n_kv_heads * w.row_tiles) * w.row_tile;
+                                    : (blocks + (size_t)d.n_kv_heads) * rows;
   const size_t own = (blocks + (size_t)d.n_kv_heads * d.batch) * group;
   Carve cv;
   w.sched = cv.take(sizeof(int) * (d.batch + 1));
-  w.pre_blocks = cv.take(sizeof(int2) * d.n_kv_heads * std::max(w.row_tiles, w.tc_groups));
+  w.pre_blocks = cv.take(sizeof(int2) * d.n_kv_heads * w.tc_groups);
   w.own_blocks = cv.take(sizeof(int2) * d.n_kv_heads * d.batch);
   w.pre_o = cv.take(pre * d.head_dim * sizeof(float));
   w.pre_ml = cv.take(pre * sizeof(float2));
@@ -753,11 +755,10 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.whole = !c.view.bt || c.view.page % kTile == 0;
   p.prefix = prefix_len;
   p.base = !c.view.bt ? prefix_len : prefix_len / (p.whole ? kTile : c.box) * (p.whole ? kTile : c.box);
-  p.row_tile = w.row_tile;
-  p.row_tiles = w.row_tiles;
-  p.tc = prefix_len > 0 && c.d.batch * p.group > kTcFrom;
+  p.rows = c.d.batch * p.group;
+  p.tc = prefix_len > 0 && p.rows > kTcFrom;
   p.tc_groups = w.tc_groups;
-  p.wide = std::max(p.group, prefix_len && !p.tc ? w.row_tile : 0) > 32;
+  p.wide = p.group > 32;
   p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * 1.44269504088896341f;
   p.q = (const uint16_t*)q;
   p.seq_lens = seq_lens;
@@ -770,7 +771,7 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.pre_ml = (float2*)(ws + w.pre_ml);
   p.own_o = (float*)(ws + w.own_o);
   p.own_ml = (float2*)(ws + w.own_ml);
-  const bool narrow = std::max(p.group, prefix_len && !p.tc ? c.d.batch * p.group : 0) <= 8;
+  const bool narrow = std::max(p.group, prefix_len && !p.tc ? p.rows : 0) <= 8;
   if (c.d.head_dim == 128) return narrow ? run<128, true>(p, c, stream) : run<128, false>(p, c, stream);
   return narrow ? run<64, true>(p, c, stream) : run<64, false>(p, c, stream);
 }

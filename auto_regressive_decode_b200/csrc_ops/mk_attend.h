@@ -13,7 +13,7 @@ struct AttendParams {
   int layer, group, box;
   int whole;               // a tile that starts at a multiple of kTile (contiguous: anywhere) is one TMA box
   int prefix, base;        // own tiles start at base: prefix rounded down so that no box crosses a page
-  int row_tile, row_tiles; // prefix rows per group, row tiles per KV head
+  int rows;                // batch * group: rows of a KV head over the prefix
   int wide;                // some piece has more than 32 rows: one query buffer
   float scale;             // scale * log2 e
   const uint16_t* q;
@@ -22,7 +22,7 @@ struct AttendParams {
   float* lse;
   int tc, tc_groups;       // the prefix runs in attend_prefix_tc: row groups of two row tiles per KV head
   // workspace
-  float *pre_o, *own_o;    // [piece][row_tile | group][hd]
+  float *pre_o, *own_o;    // [piece][rows of the piece][hd]
   float2 *pre_ml, *own_ml; // [piece][rows]
   int2 *pre_blocks, *own_blocks;  // [group] first and last block with a piece of it
   int* sched;              // [0] whether prefix groups have pieces, [1...] own tiles of each sequence
