@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   if (p.prefix && p.sched[0] == 0) r0 = make_int2(0, -1);  // no sequence reaches into the prefix: its groups have no pieces
   if (have && p.sched[1 + b] == 0) r1 = make_int2(0, -1);  // nor this sequence beyond it
   const int n0 = (r0.y - r0.x + 1) * (both ? 2 : 1), n = n0 + r1.y - r1.x + 1, step = both ? entry : per;
-  const int64_t at0 = (int64_t)(r0.x + g0) * per + (both ? row % entry : row % per), at1 = (int64_t)(r1.x + g1) * p.group + j;
+  const int first = p.tc ? tc_entry(p, p.tc_lanes > 1 ? row / per : 0, r0.x, p.tc_lanes > 1 ? kvh : g0) : r0.x + g0;
+  const int64_t at0 = (int64_t)first * per + (both ? row % entry : row % per), at1 = (int64_t)(r1.x + g1) * p.group + j;
 
   // piece i of the row: its (m, l), and its output from this lane's columns on
   const float2* ml0 = p.pre_ml + at0;
@@ -758,6 +759,8 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.rows = c.d.batch * p.group;
   p.tc = prefix_len > 0 && p.rows > kTcFrom;
   p.tc_groups = w.tc_groups;
+  p.tc_lanes = c.n_sm % w.tc_groups * 16 <= c.n_sm ? w.tc_groups : 1;  // where at most 1 SM of 16 is left without work
+  p.tc_blocks = c.n_sm / p.tc_lanes;
   p.wide = p.group > 32;
   p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * 1.44269504088896341f;
   p.q = (const uint16_t*)q;

@@ -21,6 +21,8 @@ struct AttendParams {
   uint16_t* out;
   float* lse;
   int tc, tc_groups;       // the prefix runs in attend_prefix_tc: row groups of two row tiles per KV head
+  int tc_lanes;            // tc_groups: every row group has blocks of its own; 1: they follow one another
+  int tc_blocks;           // blocks of a lane
   // workspace
   float *pre_o, *own_o;    // [piece][rows of the piece][hd]
   float2 *pre_ml, *own_ml; // [piece][rows]
@@ -33,6 +35,12 @@ __device__ __forceinline__ int active_blocks(int cost, int grid) { return min(co
 __device__ __forceinline__ int first_unit(int cost, int i, int G) {
   const int q = cost / G;
   return q * i + (cost - q * G) * i / G;
+}
+
+// A lane of attend_prefix_tc goes through its groups in order; the entry of the workspace that block i
+// of the lane leaves its piece of the lane's group k at (a piece is one more than its predecessor's).
+__device__ __forceinline__ int tc_entry(const AttendParams& p, int lane, int i, int k) {
+  return lane * (p.tc_blocks + p.c.nkv * (p.tc_groups / p.tc_lanes)) + i + k;
 }
 
 // Attention over the prefix with tcgen05 (mk_attend_tc.cu): leaves its pieces

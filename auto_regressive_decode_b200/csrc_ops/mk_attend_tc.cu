@@ -20,6 +20,10 @@
 //
 // The tiles of all groups (KV head x 256 rows) are dealt to the blocks as equal
 // contiguous runs; a piece leaves m, l and o of its rows for the join (mk_attend.cu).
+// Where the row groups of a KV head divide the SMs almost evenly, each has its own
+// blocks (a lane), so that all row groups pass over the same tiles at the same time
+// and a tile is read from memory once (65536 positions of 8 KV heads, 268 MB, for
+// 1024 rows each: 242 us instead of 274 with one order of groups for all blocks).
 //
 // Bound: the tensor cores (4 head_dim flops a row and position) and, nearly as
 // much, the exponentials (16 a clock and SM: 128 x 128 of them last as long as the
@@ -70,19 +74,20 @@ static_assert(sizeof(TcCtl) <= 512, "control block");
 // One block's run within a group.
 struct Piece {
   int kvh, row0, rows, n, t0;  // rows of the group from row0 on, tiles t0 ... t0 + n
-  int gidx;
+  int k, gidx;                 // the group in its lane, among all
   bool first, last, pair;
 };
 
 struct Walk {
-  int tiles, groups, total_rows;
+  int tiles, groups, total_rows, lane;  // lane -1: there is one
   int u, end;
   __device__ __forceinline__ bool next(Piece& a) {
     while (u < end) {
       const int n = tiles + kTcHead;
-      a.gidx = u / n;
+      a.k = u / n;
       const int r = u % n, take = min(n - r, end - u);
       u += take;
+      a.gidx = lane < 0 ? a.k : a.k * groups + lane;
       a.kvh = a.gidx / groups;
       a.row0 = a.gidx % groups * 2 * kTcRows;
       a.rows = min(2 * kTcRows, total_rows - a.row0);
@@ -152,9 +157,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // No sequence attends behind the longest: what lies there is not read.
   const int prefix_end = min(p.prefix, ctl->max_len);
   const int tiles = (prefix_end + kTcTile - 1) / kTcTile;
-  const int cost = tiles ? (tiles + kTcHead) * p.tc_groups * cv.nkv : 0;
-  const int G = active_blocks(cost, gridDim.x), cta = blockIdx.x;
-  Walk walk{tiles, p.tc_groups, cv.B * p.group, 0, 0};
+  const int cost = tiles ? (tiles + kTcHead) * (p.tc_groups / p.tc_lanes) * cv.nkv : 0;
+  const int G = active_blocks(cost, p.tc_blocks), cta = blockIdx.x / p.tc_lanes, row_lane = blockIdx.x % p.tc_lanes;
+  Walk walk{tiles, p.tc_groups, p.rows, p.tc_lanes > 1 ? row_lane : -1, 0, 0};
   if (cta < G) walk.u = first_unit(cost, cta, G), walk.end = first_unit(cost, cta + 1, G);
   Piece a;
 
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive(smem_addr(&ctl->p_full[s]));
       }
       // leave the piece
-      const int64_t entry = ((int64_t)cta + a.gidx) * 2 + s;
+      const int64_t entry = (int64_t)tc_entry(p, row_lane, cta, a.k) * 2 + s;
       if (tid == 0) {
         if (a.first) p.pre_blocks[a.gidx].x = cta;
         if (a.last) p.pre_blocks[a.gidx].y = cta;

@@ -120,6 +120,20 @@ def test_attend_matches_the_definition(case):
     check(s, out, lse)
 
 
+@pytest.mark.parametrize("case", [
+    (600, 2, 1, 128, 128, 700, [(700 + i * 7 % 91) * (i % 5 > 0) for i in range(600)]),   # 1200 rows a KV head, some idle
+    (385, 4, 2, 64, 128, 1500, [1500 + i % 9 for i in range(385)]),                       # the last two rows by themselves
+    (160, 64, 1, 64, 0, 300, [300 + i % 3 for i in range(160)]),                          # 10240 rows a KV head
+    (257, 1, 1, 128, 16, 129, [100 + i % 60 for i in range(257)]),
+], ids=lambda c: "%d rows" % (c[0] * c[1] // c[2]))
+def test_many_rows_share_a_prefix(case):
+    s = make(*case, seed=8)
+    c = handle(s)
+    out, lse = c.attend(s["layer"], s["q"], s["seq_lens"], prefix_len=s["prefix"])
+    assert c.status() == 0
+    check(s, out, lse)
+
+
 def test_sharing_changes_nothing_but_roundings():
     """The same sequences with the prefix read from sequence 0, and each with its own copy of it."""
     s = make(6, 16, 4, 128, 16, 600, [600 + 50 * i + 1 for i in range(6)], seed=2)
