@@ -186,9 +186,7 @@ extern "C" int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_ca
   w.B = d.batch;
   w.nq = d.n_q_heads;
   w.nkv = d.n_kv_heads;
-  w.hd = d.head_dim;
   w.T = d.max_ctx;
-  w.L = d.n_layers;
   w.bt = kv->block_table;
   if (w.bt) {
     w.page = kv->page_size;
@@ -216,8 +214,7 @@ extern "C" int mk_cache_destroy(mk_cache* c) {
   {
     mk::OnDevice here(c->device);
     e = cudaDeviceSynchronize();  // calls on any stream may still read the table
-    const cudaError_t f = cudaFreeAsync(c->region, cudaStreamPerThread);
-    if (e == cudaSuccess) e = f;
+    if (e == cudaSuccess) e = cudaFreeAsync(c->region, cudaStreamPerThread);  // else it stays: better lost than read after
   }
   delete c;
   return mk::launched(e);

@@ -19,7 +19,7 @@ constexpr int kWholeRows = 64;        // cache rows of a whole box of the tensor
 // What a kernel needs to find a row of the cache: contiguous
 // [L][B][nkv][T][hd], or pages [L][n_pages][nkv][page][hd] through bt[B][bt_stride].
 struct CacheView {
-  int B, nq, nkv, hd, T, L;
+  int B, nq, nkv, T;
   const int32_t* bt;
   int bt_stride, page, n_pages;
   int* status;  // [0] code, [1] detail

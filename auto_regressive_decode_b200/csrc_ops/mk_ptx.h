@@ -29,25 +29,26 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+constexpr uint32_t kTryNs = 4000;  // a try sleeps no longer
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(kTryNs)
       : "memory");
   return ok != 0;
 }
 __device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 
-// A wait is bounded by its tries (2^22, of 20 clocks and more each): it then
+// A wait is bounded by its tries (2^20, of 20 clocks to kTryNs each: between 10 ms and 5 s): it then
 // marks the block dead (`*dead`, shared memory), and every later wait of the
 // block returns soon, so that all warps reach the end of the kernel in their
 // usual order.  Counted, not timed: reading the timer woke waits up late, and its code in every wait was
 // slow to fetch where a kernel runs for microseconds.
-constexpr uint32_t kWaitTries = 1u << 22;
+constexpr uint32_t kWaitTries = 1u << 20;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {

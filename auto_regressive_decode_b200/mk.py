@@ -361,6 +361,13 @@ def _refuse(what):
     raise MkError(MK_ERR_INVALID_ARG, what)
 
 
+def _on_stream(stream, device):
+    import torch
+    if stream.device != device:
+        _refuse(f"a stream of {device} is wanted, not of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 class Cache:
     """Owns one mk_cache: the append and attend operators on a KV cache.
 
@@ -404,7 +411,7 @@ class Cache:
         q (bf16 [n][n_q][hd]) where q is given.  seq_lens int32 [B]: rows held before; starts int32 [B + 1]: the
         tokens of each sequence (None: one each); see mk_cache_append."""
         if stream is not None:
-            with self.torch.cuda.stream(stream):
+            with _on_stream(stream, self.device):
                 return self._call.append(self.h, layer, k, v, seq_lens, q, starts, positions, q_norm, k_norm, q_out)
         return self._call.append(self.h, layer, k, v, seq_lens, q, starts, positions, q_norm, k_norm, q_out)
 
@@ -413,7 +420,7 @@ class Cache:
         below prefix_len are sequence 0's for all.  Returns (out bf16 [B][n_q][hd], lse fp32 [B][n_q]); see
         mk_cache_attend."""
         if stream is not None:
-            with self.torch.cuda.stream(stream):
+            with _on_stream(stream, self.device):
                 return self._call.attend(self.h, layer, q, seq_lens, prefix_len, scale, out, lse, workspace)
         return self._call.attend(self.h, layer, q, seq_lens, prefix_len, scale, out, lse, workspace)
 
@@ -438,8 +445,7 @@ def token_logprobs(logits, tokens, top_k=0, stream=None):
     [n], entropy fp32 [n], ids int32 [n][top_k], their log probabilities fp32 [n][top_k]); see mk_token_logprobs."""
     call = _torch_calls or _calls()
     if stream is not None:
-        import torch
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits.device):
             return call.token_logprobs(logits, tokens, top_k)
     return call.token_logprobs(logits, tokens, top_k)
 

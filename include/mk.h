@@ -316,7 +316,9 @@ int mk_cache_append(mk_cache* c, int layer, const mk_append_args* args, void* st
  *   workspace device, 256-byte aligned, mk_cache_attend_bytes(c) bytes; its
  *             contents before and after the call do not matter
  * Scores, softmax sums and output sums are fp32; the probabilities are rounded
- * to bf16 as operands of the second product.
+ * to bf16 as operands of the second product.  Rows that no sequence attends may
+ * hold anything.  A NaN or infinite value in a shared row also reaches sequences
+ * that end before it (0 times it is NaN); a key does not.
  */
 int mk_cache_attend(mk_cache* c, int layer, const void* q, const int32_t* seq_lens, int prefix_len, float scale,
                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
@@ -344,7 +346,8 @@ int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_r
 
 /*
  * mk_decode_greedy with the scores of every picked token, mk_token_logprobs of
- * each step's logits.  `desc` is the one the handle was created with.
+ * each step's logits.  `desc` is the one the handle was created with
+ * (MK_ERR_INVALID_ARG where layers, batch or width differ).
  *   out_lens   device int32[batch]: the lengths after the loop (also its
  *              working state; not the array seq_lens)
  *   logits     device fp32[batch][vocab]: the last step's logits afterwards

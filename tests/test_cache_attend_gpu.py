@@ -243,3 +243,98 @@ def test_caller_buffers_and_same_bits_every_time():
     for _ in range(10):
         c.attend(1, s["q"], s["seq_lens"], prefix_len=400, out=out, lse=lse, workspace=ws)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+# ---- many rows over a shared prefix: another kernel
+
+@pytest.mark.parametrize("scale", [0.5, 3.0, -0.1])
+@pytest.mark.parametrize("batch", [20, 50])
+def test_scale_and_large_scores_of_many_rows(batch, scale):
+    s = make(batch, 8, 2, 64, 16, 300, [301 + i * 11 % 80 for i in range(batch)], seed=10, q_scale=4.0)
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=300, scale=scale)
+    check(s, out, lse, scale)
+
+
+def test_scores_that_grow_along_the_prefix():
+    """Every row's maximum is raised again and again: keys grow with the position."""
+    s = make(40, 4, 1, 128, 0, 1000, [1000 + i % 3 for i in range(40)], seed=11)
+    ramp = torch.linspace(0.05, 3, s["max_ctx"], device="cuda")[:, None]
+    s["kr"].copy_((s["kr"].abs() * ramp).bfloat16())
+    s["k"][1] = s["kr"]
+    s["q"].copy_(s["q"].abs())
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=1000)
+    check(s, out, lse)
+
+
+def test_infinite_and_nan_rows_that_many_attend_spread():
+    s = make(40, 4, 2, 64, 0, 200, [201] * 40, seed=12)
+    s["v"][1, 7, 0, 200, 3] = float("inf")          # sequence 7's own
+    s["v"][1, 0, 1, 150, 5] = float("nan")          # everyone's
+    s["k"][1, 0, 0, 60, 1] = float("nan")           # everyone's scores of one KV head
+    out, lse = handle(s).attend(1, s["q"], s["seq_lens"], prefix_len=200)
+    o = out.view(40, 2, 2, 64).clone()
+    assert torch.isnan(o[:, 0]).all() and torch.isnan(lse.view(40, 2, 2)[:, 0]).all()
+    assert torch.isnan(o[:, 1, :, 5]).all() and torch.isfinite(lse.view(40, 2, 2)[:, 1]).all()
+    o[:, 1, :, 5] = 0
+    assert torch.isfinite(o[:, 1]).all()
+
+
+def test_bad_pages_of_a_prefix_that_many_share_are_reported():
+    import auto_regressive_decode_b200.mk as mk
+    s = make(40, 4, 2, 64, 16, 200, [201] * 40, seed=13)
+    c = handle(s)
+    s["table"][0, 5] = s["k"].shape[1]
+    c.attend(1, s["q"], s["seq_lens"], prefix_len=200)
+    assert c.status() == mk.MK_ERR_RANGE
+    s["table"][0, 5] = -7
+    c.attend(1, s["q"], s["seq_lens"], prefix_len=200)
+    assert c.status() == mk.MK_ERR_RANGE and c.status() == mk.MK_OK
+
+
+def test_overlapping_calls_and_captured_graphs_of_many_rows():
+    s = make(70, 8, 2, 128, 64, 700, [700 + i % 50 for i in range(70)], seed=14)
+    c = handle(s)
+    q2 = (s["q"].float() * 0.5).bfloat16()
+    want = [c.attend(1, q, s["seq_lens"], prefix_len=700) for q in (s["q"], q2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got += [c.attend(1, q, s["seq_lens"], prefix_len=700, stream=st) for q, st in zip((s["q"], q2), streams)]
+    torch.cuda.synchronize()
+    # one workspace for the calls of a graph: they follow one another; replayed next to calls with their own
+    ws = torch.empty(c.workspace_bytes, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        inside = [c.attend(1, q, s["seq_lens"], prefix_len=700, workspace=ws) for q in (s["q"], q2)]
+    for _ in range(5):
+        with torch.cuda.stream(streams[0]):
+            g.replay()
+        got += [c.attend(1, q, s["seq_lens"], prefix_len=700, stream=streams[1]) for q in (s["q"], q2)]
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got + inside):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
+    check(s, *want[0])
+    assert c.status() == 0
+
+
+def test_a_call_right_behind_what_writes_its_inputs():
+    """Queries, lengths and rows written by the kernels just ahead on the stream, with no pause in between."""
+    s = make(40, 8, 2, 64, 0, 300, [301 + i for i in range(40)], seed=15)
+    c = handle(s)
+    want = [c.attend(1, (s["q"] * f).contiguous(), s["seq_lens"], prefix_len=300) for f in (1, 0.5, 0.25)]
+    for small in (False, True):
+        t, cc = (s, c)
+        if small:                                   # few rows: no prefix kernel
+            t = make(3, 8, 2, 64, 0, 300, [301, 305, 340], seed=16)
+            cc = handle(t)
+            want = [cc.attend(1, (t["q"] * f).contiguous(), t["seq_lens"], prefix_len=300) for f in (1, 0.5, 0.25)]
+        q, lens = torch.empty_like(t["q"]), torch.empty_like(t["seq_lens"])
+        for _ in range(20):
+            for f, w in zip((1, 0.5, 0.25), want):
+                q.copy_(t["q"]).mul_(f)
+                lens.zero_().add_(t["seq_lens"])
+                out, lse = cc.attend(1, q, lens, prefix_len=300)
+                q.zero_()                           # behind the call: not seen by it
+                lens.zero_()
+                assert torch.equal(out, w[0]) and torch.equal(lse, w[1])

@@ -76,3 +76,11 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes():
     k = torch.zeros((1, 2, 1, 8, 64), dtype=torch.bfloat16)
     with pytest.raises(mk.MkError):
         mk.Cache(k, k, n_q_heads=1, batch=2, max_ctx=8)
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+
+    import torch
+    with pytest.raises(mk.MkError, match="stream of cpu"):
+        mk.token_logprobs(torch.zeros(2, 5), torch.zeros(2, dtype=torch.int32), stream=types.SimpleNamespace(device=torch.device("cuda:1")))

@@ -146,3 +146,74 @@ def test_scored_loop_that_runs_out_of_the_cache():
     logprob, _, _, _, _ = dec.greedy_scored(steps, tok, torch.from_numpy(S0.astype(np.int32)).cuda(), picks)
     assert dec.status() == mk.MK_ERR_RANGE
     assert (picks[-2:] == -1).all() and torch.isnan(logprob[-2:]).all() and torch.isfinite(logprob[:-2]).all()
+
+
+def test_scored_loop_refuses_what_does_not_fit():
+    import auto_regressive_decode_b200.mk as mk
+    cfg = fx.CONFIGS["tiny"].replace(batch=4, ffn_dim=704, ctx=0, ctx_lo=5, ctx_hi=100)
+    S0 = fx.context_lengths(cfg)
+    kc, vc = device_caches(cfg, S0)
+    dec = mk.Decoder(cfg, device_model(cfg), kc, vc)
+    tok = torch.from_numpy(fx.tokens(cfg)[0].copy()).cuda()
+    lens = torch.from_numpy(S0.astype(np.int32)).cuda()
+    picks = torch.full((2, 4), -5, dtype=torch.int32, device="cuda")
+    for kw, code in (({"batch": 3}, mk.MK_ERR_INVALID_ARG), ({"hidden": 512}, mk.MK_ERR_INVALID_ARG), ({"n_layers": 1}, mk.MK_ERR_INVALID_ARG)):
+        dec.desc, right = mk.model_desc(cfg.replace(**kw)), dec.desc
+        with pytest.raises(mk.MkError) as e:
+            dec.greedy_scored(2, tok, lens, picks)
+        assert e.value.code == code
+        dec.desc = right
+    for k in (-1, 33):
+        with pytest.raises((mk.MkError, RuntimeError)):
+            dec.greedy_scored(2, tok, lens, picks, top_k=k)
+    torch.cuda.synchronize()
+    assert (picks == -5).all()
+    *_, end = dec.greedy_scored(0, tok, lens, picks[:0])
+    assert torch.equal(end, lens)
+
+
+def test_a_closed_cache_refuses():
+    import auto_regressive_decode_b200.mk as mk
+    k = torch.zeros((1, 2, 1, 8, 64), dtype=torch.bfloat16, device="cuda")
+    c = mk.Cache(k, k.clone(), n_q_heads=1, batch=2, max_ctx=8)
+    q, lens = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    c.attend(0, q, lens)
+    c.close()
+    c.close()
+    for f in (lambda: c.attend(0, q, lens), lambda: c.append(0, q, q, lens)):
+        with pytest.raises(mk.MkError):
+            f()
+
+
+@pytest.mark.parametrize("bad", ["layer", "q type", "q shape", "q strides", "lens type", "lens length", "prefix", "out", "workspace", "scale"])
+def test_attend_refuses(bad):
+    import auto_regressive_decode_b200.mk as mk
+    k = torch.zeros((2, 3, 2, 40, 64), dtype=torch.bfloat16, device="cuda")
+    c = mk.Cache(k, k.clone(), n_q_heads=4, batch=3, max_ctx=40)
+    a = dict(layer=1, q=torch.zeros((3, 4, 64), dtype=torch.bfloat16, device="cuda"), seq_lens=torch.ones(3, dtype=torch.int32, device="cuda"))
+    c.attend(**a)
+    a.update({"layer": {"layer": 2}, "q type": {"q": a["q"].float()}, "q shape": {"q": a["q"][:, :2].contiguous()},
+              "q strides": {"q": a["q"].transpose(0, 1).contiguous().transpose(0, 1)}, "lens type": {"seq_lens": a["seq_lens"].long()},
+              "lens length": {"seq_lens": a["seq_lens"][:2]}, "prefix": {"prefix_len": 41}, "out": {"out": a["q"].float()},
+              "workspace": {"workspace": torch.empty(c.workspace_bytes - 1, dtype=torch.uint8, device="cuda")},
+              "scale": {"scale": float("nan")}}[bad])
+    with pytest.raises(mk.MkError):
+        c.attend(**a)
+
+
+@pytest.mark.parametrize("bad", ["layer", "type", "heads", "mixed types", "tokens", "starts", "stride", "gain", "q_out", "lens"])
+def test_append_refuses(bad):
+    import auto_regressive_decode_b200.mk as mk
+    kc = torch.zeros((2, 3, 2, 40, 64), dtype=torch.bfloat16, device="cuda")
+    c = mk.Cache(kc, kc.clone(), n_q_heads=4, batch=3, max_ctx=40)
+    x = torch.zeros((3, 8, 64), device="cuda")
+    odd = torch.zeros((3, 2 * 64 + 1), device="cuda")[:, :128].view(3, 2, 64) if bad == "stride" else None
+    a = dict(layer=0, k=x[:, 4:6], v=x[:, 6:], q=x[:, :4], seq_lens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    c.append(**a)
+    a.update({"layer": {"layer": -1}, "type": {"k": a["k"].double(), "v": a["v"].double(), "q": a["q"].double()}, "heads": {"k": x[:, 3:6]},
+              "mixed types": {"v": a["v"].bfloat16()}, "tokens": {"k": x[:2, 4:6], "v": x[:2, 6:], "q": x[:2, :4]},
+              "starts": {"starts": torch.zeros(3, dtype=torch.int32, device="cuda")}, "stride": {"k": odd},
+              "gain": {"k_norm": torch.ones(64, device="cuda")}, "q_out": {"q_out": torch.empty((3, 4, 64), device="cuda")},
+              "lens": {"seq_lens": a["seq_lens"].cpu()}}[bad])
+    with pytest.raises(mk.MkError):
+        c.append(**a)
