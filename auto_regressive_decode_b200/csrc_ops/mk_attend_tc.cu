@@ -23,11 +23,14 @@
 // Where the row groups of a KV head divide the SMs almost evenly, each has its own
 // blocks (a lane), so that all row groups pass over the same tiles at the same time
 // and a tile is read from memory once (65536 positions of 8 KV heads, 268 MB, for
-// 1024 rows each: 242 us instead of 274 with one order of groups for all blocks).
+// 1024 rows each: 274 us to 242).
 //
 // Bound: the tensor cores (4 head_dim flops a row and position) and, nearly as
 // much, the exponentials (16 a clock and SM: 128 x 128 of them last as long as the
-// tile's two products); with up to about 128 rows, the cache's bytes.
+// tile's two products); with up to about 128 rows, the cache's bytes.  1024 rows of 8
+// KV heads over 65536 positions: 235 us with the join, 1170 TFLOP/s; 128 rows: 62 us,
+// 4.3 TB/s.  A stream's products and softmax alternate, about 1300 and 2000 clocks a
+// tile of 128 x 128; a third stream has no room in tensor memory.
 #include <type_traits>
 
 #include "mk_attend.h"
@@ -65,7 +68,7 @@ struct TcLayout {
 
 struct TcCtl {
   unsigned long long full[8], empty[8];
-  unsigned long long q_full, tail, s_full[2], p_full[2], o_done[2];  // [stream]
+  unsigned long long q_full, tail, s_full[2], p_half[2], p_full[2], o_done[2];  // [stream]
   uint32_t tmem;
   int dead, max_len;
 };
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(smem_addr(&ctl->tail), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&ctl->s_full[s]), 1);
+      mbar_init(smem_addr(&ctl->p_half[s]), kSoftmaxThreads / 2);
       mbar_init(smem_addr(&ctl->p_full[s]), kSoftmaxThreads / 2);
       mbar_init(smem_addr(&ctl->o_done[s]), 1);
     }
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    v_desc = smem_desc(base, kTcTile * 128, 1024);
     uint32_t at = 0;  // tiles that passed through the ring in earlier pieces
     uint32_t q_phase = 0, tail_phase = 0, p_phase = 0;
-    const uint32_t s_full = smem_addr(&ctl->s_full[s]), p_full = smem_addr(&ctl->p_full[s]), o_done = smem_addr(&ctl->o_done[s]);
+    const uint32_t s_full = smem_addr(&ctl->s_full[s]), p_half = smem_addr(&ctl->p_half[s]), p_full = smem_addr(&ctl->p_full[s]), o_done = smem_addr(&ctl->o_done[s]);
     const uint32_t s_col = tmem + kS + s * 128, o_col = tmem + kO + s * 128;
     // The streams' warps take turns.  A product is issued as the matrix unit takes it (65 to
     // 71 clocks each, a commit 40 to 75), so that whatever stands between two runs of them is
@@ -269,15 +273,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail), tail_phase, dead);
           v = v_desc + slot * (S::kSlotBytes >> 4);
           if (i + 1 < n) k = k_tile(i + 1);
-          mbar_wait(p_full, p_phase, dead);
-          p_phase ^= 1;
+          mbar_wait(p_half, p_phase, dead);
         }
         take_turn();
         tc_fence_after();
         if (i < n) {
+          // k-steps of 16 positions, 16 lines on.  The probabilities come in two parts, the first 32
+          // positions of each half and the rest, so that half of the product runs under the
+          // other half's exponentials (242 us to 235 for 65536 positions, 1024 rows of 8 KV heads).
 #pragma unroll
-          for (int ks = 0; ks < kTcTile / 16; ++ks)  // 16 lines on
-            tc_mma_ts(o_col, s_col + ks * 8, v + ks * (16 * 128 >> 4), kPv, ks > 0 || i > 0, leader);
+          for (int q = 0; q < 2; ++q) {
+            if (q) {
+              mbar_wait(p_full, p_phase, dead);
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int ks = q * 2 + e / 2 * 4 + e % 2;
+              tc_mma_ts(o_col, s_col + ks * 8, v + ks * (16 * 128 >> 4), kPv, q + e > 0 || i > 0, leader);
+            }
+          }
+          p_phase ^= 1;
           // The next scores overwrite the probabilities: after the product that reads them, in order of issue.
           if (i + 1 < n) qk(k);
           else tc_commit(o_done, leader);
@@ -397,13 +413,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             y[e] = pack_bf16x2(p0, p1);  // the operand of the second product, as the cache is
           }
           tmem_st16(s_at + c * (kHalf / 2) + q * 16, y);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_addr(q ? &ctl->p_full[s] : &ctl->p_half[s]));
         }
         float u0, u1;
         unpack2(add2(sum[0], sum[1]), u0, u1);
         l += u0 + u1;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_addr(&ctl->p_full[s]));
       }
       // leave the piece
       const int64_t entry = (int64_t)tc_entry(p, row_lane, cta, a.k) * 2 + s;
