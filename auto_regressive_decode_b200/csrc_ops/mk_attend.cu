@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   // piece i of the row: its (m, l), and its output from this lane's columns on
   const float2* ml0 = p.pre_ml + at0;
   const float2* ml1 = p.own_ml + (at1 - (int64_t)n0 * p.group);
-  const float* o0 = p.pre_o + at0 * HD + lane * V;
+  const int r0c = row % kTcRows;
+  const float* o0 = p.pre_o + (p.tc ? (at0 - r0c) * HD + TcOut<HD>::chunk(r0c, lane * V / 4) + lane * V % 4 : at0 * HD + lane * V);
   const float* o1 = p.own_o + (at1 - (int64_t)n0 * p.group) * HD + lane * V;
   float M = -INFINITY, L = 0.f, o[V] = {};
   for (int i0 = sub; i0 < n; i0 += 32 * W) {  // 32 pieces at a time: a lane's weight, then the weighted sum

@@ -43,6 +43,22 @@ __device__ __forceinline__ int tc_entry(const AttendParams& p, int lane, int i, 
   return lane * (p.tc_blocks + p.c.nkv * (p.tc_groups / p.tc_lanes)) + i + k;
 }
 
+// Where attend_prefix_tc leaves an output: float offset, within an entry of kTcRows rows, of the
+// 16-byte chunk `ch` of row r.  kTcParts blocks, [row][chunk]: of each half of the row's columns the
+// first part, the second, ...; chunks swizzled, as they lay in shared memory.
+constexpr int kTcParts = 4;
+template <int HD>
+struct TcOut {
+  static constexpr int kHalf = HD / 8, kMine = kHalf / kTcParts, kRow = 2 * kMine;  // chunks of half a row, of its part, of a row there
+  static constexpr int kFloats = kTcRows * kRow * 4;                                // a block
+  // rows r ... r + 7 of one chunk lie in different banks
+  static __device__ __forceinline__ int swizzle(int r, int ch) { return ch ^ (kRow == 8 ? r & 7 : r >> 1 & 3); }
+  static __device__ __forceinline__ int chunk(int r, int ch) {
+    const int half = ch / kHalf, part = ch % kHalf / kMine, e = ch % kMine;
+    return part * kFloats + (r * kRow + swizzle(r, half * kMine + e)) * 4;
+  }
+};
+
 // Attention over the prefix with tcgen05 (mk_attend_tc.cu): leaves its pieces
 // in pre_o / pre_ml as entries of kTcRows rows, two a piece, and the blocks of
 // every group in pre_blocks.

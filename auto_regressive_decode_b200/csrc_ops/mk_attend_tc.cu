@@ -88,11 +88,12 @@ struct Walk {
     while (u < end) {
       const int n = tiles + kTcHead;
       a.k = u / n;
-      const int r = u % n, take = min(n - r, end - u);
+      const int r = u - a.k * n, take = min(n - r, end - u);
       u += take;
-      a.gidx = lane < 0 ? a.k : a.k * groups + lane;
-      a.kvh = a.gidx / groups;
-      a.row0 = a.gidx % groups * 2 * kTcRows;
+      a.kvh = lane < 0 ? a.k / groups : a.k;
+      const int row_group = lane < 0 ? a.k - a.kvh * groups : lane;
+      a.gidx = a.kvh * groups + row_group;
+      a.row0 = row_group * 2 * kTcRows;
       a.rows = min(2 * kTcRows, total_rows - a.row0);
       a.pair = a.rows > kTcRows;
       a.t0 = max(r - kTcHead, 0);
@@ -328,19 +329,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int n = a.pair ? a.n : (a.n + 1 - s) / 2;
       const int row = (a.pair ? s * kTcRows : 0) + r;
       const bool valid = row < a.rows;
-      const int b = (a.row0 + row) / p.group, head = a.kvh * p.group + (a.row0 + row) % p.group;
+      const int b = (a.row0 + row) / p.group;
       const int lim = valid ? min(__ldg(p.seq_lens + b), prefix_end) : 0;
-      if (a.pair || s == 0) {  // half of the row's query, swizzled as TMA would
-        const uint4* q = reinterpret_cast<const uint4*>(p.q + ((int64_t)b * cv.nq + head) * HD) + c * (HD / 16);
-        uint4 x[HD / 16];
+      if (a.pair || s == 0) {  // the query tile, a thread a 16-byte chunk of every kStep-th row, swizzled as TMA would
+        constexpr int kChunks = HD / 8, kStep = 256 / kChunks;
+        const int ch = tid % kChunks, first = tid % 256 / kChunks, row0 = a.pair ? s * kTcRows : 0;
+        const int step_b = kStep / p.group, step_j = kStep % p.group;
+        int qb = (a.row0 + row0 + first) / p.group, qj = (a.row0 + row0 + first) % p.group;
+        uint4 x[kTcRows / kStep];
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) x[i] = valid ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        uint8_t* to = smem + S::kQ + (a.pair ? s : 0) * S::kQBytes + r * 128;
+        for (int i = 0; i < kTcRows / kStep; ++i) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row0 + first + i * kStep < a.rows)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)qb * cv.nq + a.kvh * p.group + qj) * HD) + ch);
+          qb += step_b;
+          qj += step_j;
+          if (qj >= p.group) qj -= p.group, ++qb;
+        }
+        uint8_t* to = smem + S::kQ + (a.pair ? s : 0) * S::kQBytes + ch / 8 * (kTcRows * 128);
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const int ch = c * (HD / 16) + i;
+        for (int i = 0; i < kTcRows / kStep; ++i) {
+          const int to_row = first + i * kStep;
           x[i].x ^= flip; x[i].y ^= flip; x[i].z ^= flip; x[i].w ^= flip;
-          *reinterpret_cast<uint4*>(to + ch / 8 * (kTcRows * 128) + (((ch % 8) ^ (r & 7)) << 4)) = x[i];
+          *reinterpret_cast<uint4*>(to + to_row * 128 + (((ch % 8) ^ (to_row & 7)) << 4)) = x[i];
         }
         fence_async_shared();
       }
@@ -435,38 +446,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         if (r == 0 && c == 0)
           mbar_arrive(smem_addr(&ctl->empty[(at + v_place(a.pair, a.pair ? n - 1 : 2 * n - 2 + s, a.n)) % S::kSlots]), a.pair ? 1 : 2);
-        // The rows' outputs pass through the query tile's memory, which is free once the
-        // stream's products are done (with one row tile, once the other stream's are too): from a
-        // thread's row to whole lines of the workspace (32 lanes' 16 bytes of 32
-        // rows took a clock a lane, 7000 clocks a piece).
+        // The outputs leave through the query tile's memory, half of them at a time, as copies
+        // of whole blocks (from each thread's row directly, 32 lanes' 16 bytes went to 32 lines: a clock
+        // a lane, 7000 a piece).  The tile is free once the stream's products are done (with one row
+        // tile, once the other stream's are too).
         if (s == 0 && !a.pair && a.n > 1) mbar_wait(smem_addr(&ctl->o_done[1]), other_phase, dead);
-        float4* stage = reinterpret_cast<float4*>(smem + S::kQ + s * S::kQBytes);
-        constexpr int kChunks = HD / 8;      // 16-byte chunks of a row in a round: half its columns
-        constexpr int kMine = kChunks / 2;   // a thread's
+        using Out = TcOut<HD>;
+        constexpr uint32_t kBytes = Out::kFloats * 4;
+        static_assert(2 * kBytes <= S::kQBytes, "two parts at a time");
         float* out = p.pre_o + entry * kTcRows * HD;
 #pragma unroll 1
-        for (int round = 0; round < 2; ++round) {
-          uint32_t y[4 * kMine];
-          if constexpr (HD == 128) tmem_ld32(o_at + round * 32, y);
-          else tmem_ld16(o_at + round * 16, y);
+        for (int part = 0; part < kTcParts; ++part) {
+          uint32_t y[4 * Out::kMine];
+          if constexpr (HD == 128) tmem_ld16(o_at + part * 16, y);
+          else tmem_ld8(o_at + part * 8, y);
           tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < kMine; ++e)
-            stage[r * kChunks + ((c * kMine + e) ^ (r & 7))] =
-                make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
-          stream_bar();
-#pragma unroll 4
-          for (int e = tid % 256; e < kTcRows * kChunks; e += 256) {
-            const int to = e / kChunks, ch = e % kChunks, half = ch / kMine;
-            if ((a.pair ? s * kTcRows : 0) + to < a.rows)
-              *reinterpret_cast<float4*>(out + to * HD + half * (HD / 2) + round * (HD / 4) + (ch % kMine) * 4) = stage[to * kChunks + (ch ^ (to & 7))];
+          const uint32_t at_part = S::kQ + s * S::kQBytes + part % 2 * kBytes;
+          if (part >= 2) {  // this memory's part before has been read
+            if (tid % 256 == 0) bulk_stores_read<1>();
+            stream_bar();
           }
+          float4* stage = reinterpret_cast<float4*>(smem + at_part) + r * Out::kRow;
+#pragma unroll
+          for (int e = 0; e < Out::kMine; ++e)
+            stage[Out::swizzle(r, c * Out::kMine + e)] =
+                make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3]));
+          fence_async_shared();
           stream_bar();
+          if (tid % 256 == 0) bulk_store(out + part * Out::kFloats, base + at_part, kBytes);
         }
+        if (tid % 256 == 0) bulk_stores_read<0>();
+        stream_bar();  // the memory is free for the next piece's queries
       }
       if (a.pair || a.n > 1) other_phase ^= 1;  // stream 1 had products in this piece
       at += 2 * a.n;
     }
+    if (tid % 256 == 0) bulk_stores_done();
   }
   tc_fence_before();
   __syncthreads();
