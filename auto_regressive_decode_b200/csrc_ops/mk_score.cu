@@ -12,9 +12,11 @@
 // top_k keys seen so far lets few keys through into a buffer; the first chunk's
 // thread maxima give the first threshold, a full buffer the next ones.  The result does not depend on the order of arrival.
 //
-// Bound: memory for many rows (one read of the logits).  Few rows: each is
-// cut over the blocks of a cluster, which join through distributed shared memory:
-// no workspace, one launch.
+// Bound: memory for many rows (one read of the logits), at half of the issue slots and of the
+// exponentials' rate: 2047 rows of 128256 bf16 logits take 116 us without alternatives (4.5
+// TB/s) and 138 with 20 (3.8 TB/s); short rows, the latency of a row's join: 2000 of 32000, 36 us.
+// Few rows: each is cut over the blocks of a cluster, which join through distributed
+// shared memory: no workspace, one launch.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -559,8 +561,11 @@ cudaError_t launch(const ScoreParams& p, int parts, int n_sm, cudaStream_t strea
 
 template <typename T>
 cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
+  // Short rows: small blocks, twice as many (2000 rows of 4096 bf16 logits, 20 alternatives: 20 us against 33;
+  // of 16000: 41 either way).
   if (p.vocab <= 4096) return launch<T, 128>(p, 1, n_sm, stream);
-  // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least.
+  // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives: one row of
+  // 128256 11.2 us, 23.8 as one block; 64 of 151936 17.5 with 4 blocks each, 28.6 with one, 29.0 with 8).
   int parts = 1;
   while (parts < 8 && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
   return launch<T, 256>(p, parts, n_sm, stream);
