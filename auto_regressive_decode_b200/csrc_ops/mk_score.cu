@@ -123,7 +123,7 @@ struct Shared {
   alignas(16) Key keys[kWarps * kRoom];  // each warp's, then all of them side by side
   Key best[kMaxTop];
   alignas(16) uint32_t tops[kGroups];
-  uint32_t raised, hint;    // upper words of limits: from the groups' maxima, and the highest that a warp found by itself
+  uint32_t raised;          // upper word of the limit
   int held[kWarps];
   int n_best, dead;
   float given;              // the given token's logit
@@ -306,7 +306,11 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
   for (int row = row0; row < p.rows; row += row_step) {
     const Part<T> r(p, row, part, parts);
     Acc acc;
-    float most = -INFINITY, lifted = -INFINITY;  // the largest logit so far; what the next reference has to exceed
+    float lifted = -INFINITY;  // what the next reference has to exceed
+    // The thread's largest chunk maximum, the second one, the rest; the chunks of the first two (as their first
+    // vector; -1: none, or the row's partial vectors, whose keys are already among the warp's).
+    float most = -INFINITY, second = -INFINITY, third = -INFINITY;
+    int where = -1, where2 = -1;
     Key limit = 0;             // keys below it are not among the best,
     float least = -3.402823466e38f;  // nor are logits below this one
     auto set_limit = [&](Key to) {
@@ -318,7 +322,6 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     int held = 0;   // keys of this warp
     float given = NAN;
     if (tid == 0 && parts == 1) given = given_logit<T>(p, r.x, row);
-    if (tid == 0) sh.hint = 0;
     // the keys of a warp, a lane each (0: none), into its room; a full room is cut to its k best
     auto push = [&](Key key) {
       const bool pass = key != 0 && key >= limit;
@@ -339,7 +342,6 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
         __syncwarp();
         held = k;  // more than 32 keys were held
         set_limit(mine[k - 1] + 1);
-        if (lane == 0) atomicMax(&sh.hint, (uint32_t)(limit >> 32));
       }
       if (pass) mine[held + __popc(who & ((1u << lane) - 1))] = key;
       held += n;
@@ -358,8 +360,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       if (k > 0) push(f > -INFINITY ? make_key(f, i) : 0);
     }
 
-    int chunk = 0, next_raise = 0;
-    for (int v0 = r.v0; v0 < r.v1; v0 += CH, ++chunk) {
+    for (int v0 = r.v0; v0 < r.v1; v0 += CH) {
       mbar_wait(smem_addr(&sh.full[slot]), phase, dead);
       const T* here = reinterpret_cast<const T*>(sh.ring[slot]);
       uint4 raw[U];
@@ -367,13 +368,23 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       for (int u = 0; u < U; ++u) {
         raw[u] = reinterpret_cast<const uint4*>(here)[u * NT + tid];
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+      if (++slot == kStagesS) slot = 0, phase ^= 1;
       if (v0 + CH > r.v1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (v0 + u * NT + tid >= r.v1) raw[u] = Vec<T>::none();
       }
       const float top = Vec<T>::top(raw);
-      most = fmaxf(most, top);
+      if (k > 0) {
+        const bool first = top > most, next = top > second;
+        third = fmaxf(third, next ? second : top);
+        second = first ? most : (next ? top : second);
+        where2 = first ? where : (next ? v0 : where2);
+        most = first ? top : most;
+        where = first ? v0 : where;
+      }
       if (top > lifted) acc.lift(top, lifted);
       F2 z2 = pack2(0.f, 0.f), s2 = z2;
       const F2 back = pack2(-acc.c, -acc.c), scale = pack2(kLog2e, kLog2e);
@@ -413,82 +424,96 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       }
       acc.z += z;
       acc.s += s;
-
-      if (k > 0) {
-        if (chunk == next_raise && (chunk == 0 || v0 + CH < r.v1)) {
-          // After chunks 1, 2, 4, ... (but not the last): raise the limit to the k-th
-          // largest maximum of the thread groups so far, which k keys reach; a
-          // group's threads share the comparisons of its maximum with the others.
-          next_raise = 2 * chunk + 1;
-          constexpr int GT = NT / kGroups;
-          uint32_t g = most > -INFINITY ? ordered(most) & ~(kGroups - 1u) : 0u;
-#pragma unroll
-          for (int o = GT / 2; o; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-          g |= tid / GT;  // no two are equal; a limit that is too low by less than kGroups steps is still one
-          if (tid % GT == 0) sh.tops[tid / GT] = g;
-          compute_bar<NT>();
-          int rank = 0;
-#pragma unroll
-          for (int i = 0; i < kGroups / GT; i += 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(sh.tops + tid % GT * (kGroups / GT) + i);
-            rank += (w.x > g) + (w.y > g) + (w.z > g) + (w.w > g);
-          }
-#pragma unroll
-          for (int o = GT / 2; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-          if (rank == k - 1 && tid % GT == 0) sh.raised = g & ~(kGroups - 1u);
-          compute_bar<NT>();
-          set_limit((Key)max(sh.raised, *(volatile uint32_t*)&sh.hint) << 32);
-        }
-        // the warp looks through its candidates, a lane a logit: one at a time, or two whose 16 logits fill a half warp each
-        uint32_t todo = __ballot_sync(0xffffffffu, top >= least);
-        while (todo) {
-          constexpr int kMine = U * VEC;  // logits of a thread
-          int t = __ffs(todo) - 1;
-          todo &= todo - 1;
-          bool there = true;
-          if (kMine < 32 && lane >= kMine) {
-            t = __ffs(todo) - 1;
-            there = t >= 0;
-          }
-          if (kMine < 32) todo &= todo - 1;
-          const int at = lane % kMine, u = at / VEC, i = at % VEC, v = v0 + u * NT + (tid & ~31) + t;
-          Key key = 0;
-          if (there && v < r.v1) {
-            const float f = Vec<T>::one(here[(v - v0) * VEC + i]);
-            if (f > -INFINITY) key = make_key(f, v * VEC - r.skew + i);
-          }
-          push(key);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
-      if (++slot == kStagesS) slot = 0, phase ^= 1;
     }
 
-    // join the warps' sums and keys
+    // the warps' sums; a limit of the keys: the k-th largest maximum of the thread groups, which k keys reach
     Sum a = warp_join(acc.sum());
-    if (lane == 0) {
-      sh.part[warp] = a;
-      sh.held[warp] = held;
-    }
-    const Key ka = lane < held ? mine[lane] : 0, kb = lane + 32 < held ? mine[lane + 32] : 0;
-    compute_bar<NT>();
-    int n = 0, before = 0;
+    if (lane == 0) sh.part[warp] = a;
+    constexpr int GT = NT / kGroups;
+    uint32_t g = 0;
+    if (k > 0) {
+      g = most > -INFINITY ? ordered(most) & ~(kGroups - 1u) : 0u;
 #pragma unroll
-    for (int w = 0; w < S::kWarps; ++w) {
-      if (w == warp) before = n;
-      n += sh.held[w];
+      for (int o = GT / 2; o; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+      g |= tid / GT;  // no two are equal; a limit that is too low by less than kGroups steps is still one
+      if (tid % GT == 0) sh.tops[tid / GT] = g;
     }
-    if (lane < held) sh.keys[before + lane] = ka;
-    if (lane + 32 < held) sh.keys[before + lane + 32] = kb;
+    compute_bar<NT>();
     if (warp == 0) {
       a = warp_join(lane < S::kWarps ? sh.part[lane] : Sum{-INFINITY, 0.f, 0.f});
       if (lane == 0) sh.sum = a;
     }
-    compute_bar<NT>();
-    int got = min(n, k);
-    rank_keys(sh.keys, n, k, sh.best, tid, NT);
-    if (tid == 0) sh.n_best = got;
+    int n = 0, got = 0;
+    if (k > 0) {
+      int rank = 0;  // a group's threads share the comparisons of its maximum with the others
+#pragma unroll
+      for (int i = 0; i < kGroups / GT; i += 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(sh.tops + tid % GT * (kGroups / GT) + i);
+        rank += (w.x > g) + (w.y > g) + (w.z > g) + (w.w > g);
+      }
+#pragma unroll
+      for (int o = GT / 2; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (rank == k - 1 && tid % GT == 0) sh.raised = g & ~(kGroups - 1u);
+      compute_bar<NT>();
+      set_limit((Key)sh.raised << 32);
+      // The warp looks through the chunks whose maxima reach the limit, read once more: a lane a logit of one thread's
+      // share, or of two whose 16 logits fill a half warp each; several shares' loads under way at once.
+      constexpr int kMine = U * VEC, kAtOnce = 32 / kMine, kAhead = 4;
+      const int at = lane % kMine, u = at / VEC, i = at % VEC;
+      auto look = [&](uint32_t todo, int from) {
+        while (todo) {
+          float f[kAhead];
+          int index[kAhead];
+#pragma unroll
+          for (int q = 0; q < kAhead; ++q) {
+            int t = __ffs(todo) - 1;
+            todo &= todo - 1;
+            if (kAtOnce == 2) {
+              const int t2 = __ffs(todo) - 1;
+              todo &= todo - 1;
+              if (lane >= kMine) t = t2;
+            }
+            const int v = __shfl_sync(0xffffffffu, from, t & 31) + u * NT + (tid & ~31) + t;
+            f[q] = -INFINITY;
+            index[q] = v * VEC - r.skew + i;
+            if (t >= 0 && v < r.v1) f[q] = Vec<T>::one(r.x[index[q]]);
+          }
+#pragma unroll
+          for (int q = 0; q < kAhead; ++q) push(f[q] > -INFINITY ? make_key(f[q], index[q]) : 0);
+        }
+      };
+      look(__ballot_sync(0xffffffffu, where >= 0 && most >= least), where);
+      look(__ballot_sync(0xffffffffu, where2 >= 0 && second >= least), where2);
+      // a thread with more than two such chunks (a row of 20 in some): its others are looked for, a lane a chunk
+      for (uint32_t more = __ballot_sync(0xffffffffu, third >= least); more; more &= more - 1) {
+        const int t = __ffs(more) - 1, known = __shfl_sync(0xffffffffu, where, t), known2 = __shfl_sync(0xffffffffu, where2, t);
+        for (int v0 = r.v0; v0 < r.v1; v0 += 32 * CH) {
+          const int mine0 = v0 + lane * CH, v = mine0 + (tid & ~31) + t;
+          uint4 raw[U];
+#pragma unroll
+          for (int w = 0; w < U; ++w)
+            raw[w] = v + w * NT < r.v1 ? __ldg(reinterpret_cast<const uint4*>(r.x - r.skew) + v + w * NT) : Vec<T>::none();
+          const float top = Vec<T>::top(raw);
+          uint32_t hit = __ballot_sync(0xffffffffu, top >= least && mine0 != known && mine0 != known2);
+          for (; hit; hit &= hit - 1) look(1u << t, v0 + (__ffs(hit) - 1) * CH);
+        }
+      }
+      if (lane == 0) sh.held[warp] = held;
+      const Key ka = lane < held ? mine[lane] : 0, kb = lane + 32 < held ? mine[lane + 32] : 0;
+      compute_bar<NT>();
+      int before = 0;
+#pragma unroll
+      for (int w = 0; w < S::kWarps; ++w) {
+        if (w == warp) before = n;
+        n += sh.held[w];
+      }
+      if (lane < held) sh.keys[before + lane] = ka;
+      if (lane + 32 < held) sh.keys[before + lane + 32] = kb;
+      compute_bar<NT>();
+      got = min(n, k);
+      rank_keys(sh.keys, n, k, sh.best, tid, NT);
+      if (tid == 0) sh.n_best = got;
+    }
     compute_bar<NT>();
 
     if (parts > 1) {  // one row a cluster
@@ -528,7 +553,6 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
         p.tops[(int64_t)row * k + tid] = none ? NAN : (has ? from_ordered((uint32_t)(key >> 32)) - q.m - lnz : -INFINITY);
       }
     }
-    compute_bar<NT>();  // the shared sums and keys are free for the next row
   }
 }
 
