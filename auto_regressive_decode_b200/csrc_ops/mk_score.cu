@@ -8,13 +8,17 @@
 //
 // Alternatives: a key packs the order-preserving map of the logit over the
 // inverted index, so that the largest key is the largest logit, of the lowest
-// index among equals, and no two keys are equal.  A threshold below at least
-// top_k keys seen so far lets few keys through into a buffer; the first chunk's
-// thread maxima give the first threshold, a full buffer the next ones.  The result does not depend on the order of arrival.
+// index among equals, and no two keys are equal.  On the way a thread keeps only its
+// largest maxima of a chunk and where they were.  At the row's end the k-th largest of
+// the thread groups' maxima is a limit that k keys reach; the few chunk shares that
+// reach it are read once more and their keys ranked.  (Candidates collected on the
+// way, against a limit raised after chunks 1, 2, 4, ..., cost two barriers a raise and the slower
+// the later the best ones came: 137 us for the 2047 rows below, 310 for 444 ascending ones, now 38.)
+// The result does not depend on the order of arrival.
 //
 // Bound: memory for many rows (one read of the logits), at half of the issue slots and of the
-// exponentials' rate: 2047 rows of 128256 bf16 logits take 116 us without alternatives (4.5
-// TB/s) and 138 with 20 (3.8 TB/s); short rows, the latency of a row's join: 2000 of 32000, 36 us.
+// exponentials' rate: 2047 rows of 128256 bf16 logits take 96 us without alternatives (5.5
+// TB/s) and 117 with 20 (4.5 TB/s); short rows, the latency of a row's join: 2000 of 32000 bf16 35 and 53 us.
 // Few rows: each is cut over the blocks of a cluster, which join through distributed
 // shared memory: no workspace, one launch.
 #include <cooperative_groups.h>
@@ -122,7 +126,7 @@ struct Shared {
   unsigned long long full[kStagesS], empty[kStagesS];
   alignas(16) Key keys[kWarps * kRoom];  // each warp's, then all of them side by side
   Key best[kMaxTop];
-  alignas(16) uint32_t tops[kGroups];
+  alignas(16) uint32_t tops[NT];  // the threads' maxima
   uint32_t raised;          // upper word of the limit
   int held[kWarps];
   int n_best, dead;
@@ -307,10 +311,10 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     const Part<T> r(p, row, part, parts);
     Acc acc;
     float lifted = -INFINITY;  // what the next reference has to exceed
-    // The thread's largest chunk maximum, the second one, the rest; the chunks of the first two (as their first
-    // vector; -1: none, or the row's partial vectors, whose keys are already among the warp's).
+    // The thread's largest chunk maximum and the two next ones, each the first of equal ones; their chunks (as first
+    // vectors; -1: none, or the row's partial vectors, whose keys are already among the warp's).
     float most = -INFINITY, second = -INFINITY, third = -INFINITY;
-    int where = -1, where2 = -1;
+    int where = -1, where2 = -1, where3 = -1;
     Key limit = 0;             // keys below it are not among the best,
     float least = -3.402823466e38f;  // nor are logits below this one
     auto set_limit = [&](Key to) {
@@ -379,7 +383,9 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       const float top = Vec<T>::top(raw);
       if (k > 0) {
         const bool first = top > most, next = top > second;
-        third = fmaxf(third, next ? second : top);
+        const bool last = next ? second >= third : top > third;  // what is second now came before an equal third
+        where3 = last ? (next ? where2 : v0) : where3;
+        third = last ? (next ? second : top) : third;
         second = first ? most : (next ? top : second);
         where2 = first ? where : (next ? v0 : where2);
         most = first ? top : most;
@@ -430,14 +436,10 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     Sum a = warp_join(acc.sum());
     if (lane == 0) sh.part[warp] = a;
     constexpr int GT = NT / kGroups;
-    uint32_t g = 0;
-    if (k > 0) {
-      g = most > -INFINITY ? ordered(most) & ~(kGroups - 1u) : 0u;
-#pragma unroll
-      for (int o = GT / 2; o; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-      g |= tid / GT;  // no two are equal; a limit that is too low by less than kGroups steps is still one
-      if (tid % GT == 0) sh.tops[tid / GT] = g;
-    }
+    // Thread t is of group t % kGroups: the threads that have a part of a short row are in different ones (300 bf16 logits,
+    // 20 alternatives: neighbours in one group left fewer than 20 groups and no limit, 12 us against 8).  No two
+    // groups' values are equal; a limit that is too low by less than kGroups steps is still one.
+    sh.tops[tid] = (most > -INFINITY ? ordered(most) & ~(kGroups - 1u) : 0u) | tid % kGroups;
     compute_bar<NT>();
     if (warp == 0) {
       a = warp_join(lane < S::kWarps ? sh.part[lane] : Sum{-INFINITY, 0.f, 0.f});
@@ -445,10 +447,19 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     }
     int n = 0, got = 0;
     if (k > 0) {
-      int rank = 0;  // a group's threads share the comparisons of its maximum with the others
+      // GT threads share the comparisons of a group's maximum with the others (each from another bank on)
+      uint32_t g = 0;
+#pragma unroll
+      for (int q = 0; q < GT; ++q) g = max(g, sh.tops[q * kGroups + tid / GT]);
+      int rank = 0;
 #pragma unroll
       for (int i = 0; i < kGroups / GT; i += 4) {
-        const uint4 w = *reinterpret_cast<const uint4*>(sh.tops + tid % GT * (kGroups / GT) + i);
+        uint4 w = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < GT; ++q) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sh.tops + q * kGroups + tid % GT * (kGroups / GT) + ((i + tid % GT * 4) & (kGroups / GT - 1)));
+          w = make_uint4(max(w.x, x.x), max(w.y, x.y), max(w.z, x.z), max(w.w, x.w));
+        }
         rank += (w.x > g) + (w.y > g) + (w.z > g) + (w.w > g);
       }
 #pragma unroll
@@ -482,10 +493,14 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
           for (int q = 0; q < kAhead; ++q) push(f[q] > -INFINITY ? make_key(f[q], index[q]) : 0);
         }
       };
-      look(__ballot_sync(0xffffffffu, where >= 0 && most >= least), where);
-      look(__ballot_sync(0xffffffffu, where2 >= 0 && second >= least), where2);
-      // a thread with more than two such chunks (a row of 20 in some): its others are looked for, a lane a chunk
-      for (uint32_t more = __ballot_sync(0xffffffffu, third >= least); more; more &= more - 1) {
+      // whether this thread's share of a chunk, or of a later one of no larger maximum, can hold a key to be kept
+      auto reaches = [&](float top, int v0) {
+        return top >= least && make_key(top, max((v0 + tid) * VEC - r.skew, 0)) >= limit;
+      };
+      look(__ballot_sync(0xffffffffu, where >= 0 && reaches(most, where)), where);
+      look(__ballot_sync(0xffffffffu, where2 >= 0 && reaches(second, where2)), where2);
+      // a thread with more than two such chunks (one row of 20 has one): its others are looked for, a lane a chunk
+      for (uint32_t more = __ballot_sync(0xffffffffu, reaches(third, where3)); more; more &= more - 1) {
         const int t = __ffs(more) - 1, known = __shfl_sync(0xffffffffu, where, t), known2 = __shfl_sync(0xffffffffu, where2, t);
         for (int v0 = r.v0; v0 < r.v1; v0 += 32 * CH) {
           const int mine0 = v0 + lane * CH, v = mine0 + (tid & ~31) + t;
@@ -585,11 +600,12 @@ cudaError_t launch(const ScoreParams& p, int parts, int n_sm, cudaStream_t strea
 
 template <typename T>
 cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
-  // Short rows: small blocks, twice as many (2000 rows of 4096 bf16 logits, 20 alternatives: 20 us against 33;
-  // of 16000: 41 either way).
-  if (p.vocab <= 4096) return launch<T, 128>(p, 1, n_sm, stream);
-  // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives: one row of
-  // 128256 11.2 us, 23.8 as one block; 64 of 151936 17.5 with 4 blocks each, 28.6 with one, 29.0 with 8).
+  // More rows than large blocks fit the SMs, and not long: small blocks, twice as many (20 alternatives of bf16
+  // rows: 500 of 4096 8.5 us against 13.2, 2000 of 16000 34 against 37, of 32000 53 against 52, of 50257 72 against 74;
+  // 200 of 32000 13.0 against 10.7).
+  if (p.rows > 3 * n_sm && p.vocab <= 32768) return launch<T, 128>(p, 1, n_sm, stream);
+  // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives of fp32 rows: one of
+  // 128256 10.4 us, 18.0 as one block; 64 of 151936 14.8 with 4 blocks each, 22.5 with one, 25.6 with 8).
   int parts = 1;
   while (parts < 8 && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
   return launch<T, 256>(p, parts, n_sm, stream);

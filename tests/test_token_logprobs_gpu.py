@@ -105,6 +105,29 @@ def test_special_rows(kind, rows, vocab):
     check(x, torch.randint(vocab, (rows,), generator=g, device="cuda", dtype=torch.int32), 20)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("order", ["up", "down", "equal", "random", "pairs", "late pair"])
+@pytest.mark.parametrize("rows,vocab,step", [(5, 151936, 8192), (5, 70003, 4096), (300, 70003, 4096), (7, 3500, 1024)])
+def test_the_best_lie_a_fixed_step_apart(order, rows, vocab, step, dtype):
+    """All of them in the share of few threads."""
+    g = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn((rows, vocab), generator=g, device="cuda")
+    at = torch.arange(41, vocab, step, device="cuda")
+    n = torch.arange(len(at), device="cuda")
+    value = {"up": n, "down": -n, "equal": n * 0, "random": torch.randint(0, 4, (len(at),), generator=g, device="cuda"), "pairs": -(n // 2),
+             "late pair": (n >= len(at) - 2).int()}[order]
+    x[:, at] = 50 + value.float()
+    x[1::2] = x[1::2].roll(3, 1)
+    check(x.to(dtype), torch.randint(vocab, (rows,), generator=g, device="cuda", dtype=torch.int32), 20)
+
+
+@pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "two values", "zeros of both signs", "few allowed", "tail allowed", "far", "one"])
+def test_special_rows_of_bf16(kind):
+    g = torch.Generator("cuda").manual_seed(6)
+    x = special(kind, 3, 100003, g).bfloat16()
+    check(x, torch.randint(100003, (3,), generator=g, device="cuda", dtype=torch.int32), 32)
+
+
 def test_huge_logits_do_not_overflow():
     import auto_regressive_decode_b200.mk as mk
     g = torch.Generator("cuda").manual_seed(3)
