@@ -5,8 +5,9 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain
 //   out[i]     = y[i] cos a_i - y[i + hd/2] sin a_i
 //   out[i + h] = y[i + hd/2] cos a_i + y[i] sin a_i,   a_i = pos theta^(-2i/hd)
-// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 230 us, 6.6
-// TB/s; 4100 of 48 bf16 rows 17.7 us, 5.7 TB/s; one token of each of 8 sequences 2.4 us, a launch.
+// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 234 us, 6.5
+// TB/s; 4100 of 48 bf16 rows 21.5 us, 4.7 TB/s (the latency of finding a token's place; 17.7 with the
+// rows in the L2 cache); one token of each of 8 sequences 2.6 us, a launch.
 // hd/16 neighbouring lanes hold a row, each 8 values of its first half and the 8
 // they pair with, so that loads and stores are 16 bytes and a lane's cos/sin (8
 // pairs) serve all its rows of the token.
@@ -62,9 +63,10 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
 // the first.  A token's place takes three loads that wait for each other; what
 // hides them is the number of resident blocks, hence few threads and registers a
 // block: 16000 tokens of 32 rows of 64 took 43 us with 32 slots and R = 4, 25 us with 16 and 2.
-// Tokens of many rows want the larger block: 16384 of 120 fp32 rows of 128 245 us with 16 slots, 230 with 32.
+// Tokens of many rows want the larger block: 16384 of 120 fp32 rows of 128 245 us with 16 slots, 230 with 32
+// (at 128 registers: two blocks an SM; the compiler's own choice, 140, took 144 us instead of 101 for 6000 with norms).
 template <typename T, int HD, int kSlots, int R>
-__global__ void __launch_bounds__(kSlots * HD / 16) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots * HD / 16) : 0) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = HD / 16;              // lanes of a row
   constexpr int kThreadsA = kSlots * kLanes;
   const CacheView& c = p.c;
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kSlots * HD / 16) append_kernel(const __grid_c
         for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const uint16_t* gain = h < nq ? p.q_norm : (h < nq + c.nkv ? p.k_norm : nullptr);
         if (gain && h < nh) {
-          const float inv = 1.0f / sqrtf(ss * (1.0f / HD) + p.eps);
+          const float inv = rsqrtf(ss * (1.0f / HD) + p.eps);  // off by 2^-22 at most: a root and a division took 5 to 10 % of the call
           Vec8<uint16_t> ga, gb;
           ga.a = __ldg(reinterpret_cast<const uint4*>(gain + lane * 8));
           gb.a = __ldg(reinterpret_cast<const uint4*>(gain + HD / 2 + lane * 8));
