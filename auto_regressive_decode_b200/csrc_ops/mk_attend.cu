@@ -62,6 +62,7 @@ struct Layout {
   static constexpr int kCtl = kMl + kWarps * 16 * 8;
   static constexpr int kLens = kCtl + 256;                  // int[batch], then int[batch + 1]: cost of the sequences before
   static constexpr int total(int batch) { return kLens + (2 * batch + 1) * 4 + 1024; }  // 1024: the ring is aligned by hand
+  static_assert(NARROW || kTcFrom <= kQRows, "the rows over a prefix");
   static_assert(kLens + 2048 + 1024 <= 227 * 1024 / kBlocksPerSm - 1024, "blocks an SM");
 };
 

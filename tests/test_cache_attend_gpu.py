@@ -338,3 +338,73 @@ def test_a_call_right_behind_what_writes_its_inputs():
                 q.zero_()                           # behind the call: not seen by it
                 lens.zero_()
                 assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("batch", [3, 40])
+def test_inputs_from_another_stream_and_from_copies(batch):
+    """What is ahead of the call: a wait for another stream's kernels, a copy; on the stream and in a captured graph."""
+    s = make(batch, 8, 2, 64, 16, 300, [301 + 3 * i for i in range(batch)], seed=17)
+    c = handle(s)
+    factors = (1, 0.5, 0.25, 2)
+    want = [c.attend(1, (s["q"] * f).contiguous(), s["seq_lens"], prefix_len=300) for f in factors]
+    src, q, lens = s["q"].clone(), torch.empty_like(s["q"]), torch.empty_like(s["seq_lens"])
+    big = torch.zeros(1 << 24, device="cuda")
+    side = torch.cuda.Stream()
+
+    def call():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            big.add_(1)                             # long enough that a missing wait would show
+            lens.copy_(s["seq_lens"])
+            q.copy_(src)
+        big[:1 << 20].mul_(0.5)
+        main.wait_stream(side)
+        first = c.attend(1, q, lens, prefix_len=300)
+        q.zero_()
+        q.copy_(src)                                # a copy just ahead
+        return first, c.attend(1, q, lens, prefix_len=300)
+
+    def compare(got, i):
+        for out, lse in got:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i
+    for i, f in enumerate(factors):
+        src.copy_(s["q"]).mul_(f)
+        lens.zero_()
+        compare(call(), i)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        inside = call()
+    for _ in range(3):
+        for i, f in enumerate(factors):
+            src.copy_(s["q"]).mul_(f)
+            lens.zero_()
+            q.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            compare(inside, i)
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("case", [
+    (1, 16, 8, 128, 0, 1000, [1024]), (7, 12, 4, 64, 16, 777, [800 + 40 * i for i in range(7)]), (9, 32, 8, 128, 64, 600, [601] * 9),
+    (33, 64, 2, 128, 0, 130, [200] * 33), (300, 4, 4, 64, 32, 65, [66 + i % 40 for i in range(300)]), (200, 8, 2, 128, 128, 2000, [2001] * 200),
+], ids=lambda c: "%d of %d/%d heads" % c[:3])
+def test_nothing_is_written_outside_the_callers_buffers(case):
+    s = make(*case, seed=18)
+    c = handle(s)
+    batch, nq, hd = s["q"].shape
+
+    def fenced(nbytes):
+        whole = torch.full((nbytes + 2 * 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        return whole, whole[4096:4096 + nbytes]
+    parts = [fenced(n) for n in (c.workspace_bytes, batch * nq * hd * 2, batch * nq * 4)]
+    k0, v0 = s["k"].clone(), s["v"].clone()
+    out, lse = parts[1][1].view(torch.bfloat16).view(batch, nq, hd), parts[2][1].view(torch.float32).view(batch, nq)
+    for _ in range(2):
+        c.attend(s["layer"], s["q"], s["seq_lens"], prefix_len=s["prefix"], out=out, lse=lse, workspace=parts[0][1])
+    check(s, out, lse)
+    for whole, _ in parts:
+        assert (whole[:4096] == 0xA5).all() and (whole[-4096:] == 0xA5).all()
+    assert torch.equal(s["k"].view(torch.int16), k0.view(torch.int16)) and torch.equal(s["v"].view(torch.int16), v0.view(torch.int16))

@@ -217,3 +217,32 @@ def test_append_refuses(bad):
               "lens": {"seq_lens": a["seq_lens"].cpu()}}[bad])
     with pytest.raises(mk.MkError):
         c.append(**a)
+
+
+@pytest.mark.parametrize("batch", [4, 30])
+def test_far_pages_of_a_large_pool_equal_near_ones(batch):
+    """Rows whose element offsets pass 2^32, against the same rows in a small pool: bit for bit."""
+    import auto_regressive_decode_b200.mk as mk
+    g = torch.Generator("cuda").manual_seed(9)
+    nq, nkv, hd, page, far = 16, 8, 128, 64, 68000
+    P, own = 200, 70
+    stride = -(-(P + own) // page)
+    max_ctx = stride * page
+    small = torch.randperm(batch * stride, generator=g, device="cuda").int().view(batch, stride).contiguous()
+    outs = []
+    x = torch.randn((P + batch * own, nq + 2 * nkv, hd), generator=g, device="cuda").bfloat16()
+    for pool, table in ((batch * stride, small), (far + batch * stride, small + far)):
+        k, v = (torch.empty((1, pool, nkv, page, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        assert pool < far or k.numel() > 2 ** 32
+        c = mk.Cache(k, v, n_q_heads=nq, batch=batch, max_ctx=max_ctx, block_table=table.contiguous(), page_size=page)
+        zero = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        first = torch.tensor([0] + [P] * batch, dtype=torch.int32, device="cuda")
+        c.append(0, x[:P, nq:nq + nkv], x[:P, nq + nkv:], zero, starts=first)
+        rest = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * own
+        q = c.append(0, x[P:, nq:nq + nkv], x[P:, nq + nkv:], zero + P, q=x[P:, :nq], starts=rest)
+        outs.append((q, *c.attend(0, q.view(batch, own, nq, hd)[:, -1].contiguous(), zero + P + own, prefix_len=P)))
+        assert c.status() == mk.MK_OK
+        c.close()
+        del k, v
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and not torch.isnan(a).any()

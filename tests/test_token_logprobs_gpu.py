@@ -177,3 +177,33 @@ def test_no_rows_and_captured_calls():
     g.replay()
     torch.cuda.synchronize()
     check(x, tok, 3, out)
+
+
+def test_calls_on_several_streams_and_the_same_bits_every_time():
+    import auto_regressive_decode_b200.mk as mk
+    g = torch.Generator("cuda").manual_seed(7)
+    work = []
+    for rows, vocab, dtype in ((1, 128256, torch.float32), (600, 5000, torch.bfloat16), (20, 151936, torch.bfloat16), (5, 333, torch.float32)):
+        x = (torch.randn((rows, vocab), generator=g, device="cuda") * 3).to(dtype)
+        tok = torch.randint(vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+        work.append((x, tok, mk.token_logprobs(x, tok, top_k=17)))
+        check(x, tok, 17, work[-1][2])
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for st, (x, tok, _) in zip(streams, work):
+            got.append(mk.token_logprobs(x, tok, top_k=17, stream=st))
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        for a, b in zip(r, work[i % len(work)][2]):
+            assert torch.equal(a, b)
+
+
+def test_a_row_read_many_times_and_rows_of_one_buffer():
+    """Row stride 0, and rows that overlap: they are only read."""
+    g = torch.Generator("cuda").manual_seed(8)
+    x = torch.randn(9000, generator=g, device="cuda")
+    tok = torch.randint(8000, (6,), generator=g, device="cuda", dtype=torch.int32)
+    check(x[:8000].expand(6, 8000), tok, 5)
+    check(x.as_strided((6, 8000), (100, 1)), tok, 5)
