@@ -117,6 +117,7 @@ struct Vec<uint16_t> {
 constexpr int kStagesS = 4;   // chunks in flight, each NT * kVecs vectors
 constexpr int kGroups = 64;   // thread groups whose maxima raise the limit
 constexpr int kRoom = 64;     // keys a warp holds
+constexpr int kMaxParts = 8;  // blocks of a cluster
 
 // NT compute threads and a producer warp.
 template <int NT>
@@ -167,6 +168,27 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int k, Key* be
     }
     if (n & 1) rank += keys[n - 1] > a;
     if (t < n && rank < k) best[rank] = a;
+  }
+}
+
+// Largest k of the keys of `parts` sorted lists of k, side by side at `keys`, sorted, to `best` (not `keys`
+// itself): a key's rank is the number of larger ones in every list, found by halving in all lists at once.
+__device__ __forceinline__ void merge_keys(const Key* keys, int parts, int k, Key* best, int t, int nt) {
+  for (; t < parts * k; t += nt) {
+    const Key a = keys[t];
+    int larger[kMaxParts] = {};
+#pragma unroll 1
+    for (int step = 1 << (31 - __clz(k)); step; step >>= 1) {  // the first `larger` keys of a list are known to be larger
+#pragma unroll
+      for (int l = 0; l < kMaxParts; ++l) {
+        const int at = larger[l] + step;
+        if (l < parts && at <= k && keys[l * k + at - 1] > a) larger[l] = at;
+      }
+    }
+    int rank = 0;
+#pragma unroll
+    for (int l = 0; l < kMaxParts; ++l) rank += larger[l];
+    if (a && rank < k) best[rank] = a;
   }
 }
 
@@ -527,6 +549,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       compute_bar<NT>();
       got = min(n, k);
       rank_keys(sh.keys, n, k, sh.best, tid, NT);
+      if (tid >= n && tid < k) sh.best[tid] = 0;
       if (tid == 0) sh.n_best = got;
     }
     compute_bar<NT>();
@@ -540,14 +563,11 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
         }
         // the blocks' best keys side by side (0 where one has fewer), one remote read a thread
         n = parts * k;
-        for (int i = tid; i < n; i += NT) {
-          const S* o = cluster.map_shared_rank(&sh, i / k);
-          sh.keys[i] = i % k < o->n_best ? o->best[i % k] : 0;
-        }
+        for (int i = tid; i < n; i += NT) sh.keys[i] = cluster.map_shared_rank(&sh, i / k)->best[i % k];
         got = lane < parts ? cluster.map_shared_rank(&sh, lane)->n_best : 0;
         got = min(__reduce_add_sync(0xffffffffu, got), k);
         compute_bar<NT>();
-        rank_keys(sh.keys, n, k, sh.best, tid, NT);
+        merge_keys(sh.keys, parts, k, sh.best, tid, NT);
         compute_bar<NT>();
       }
       cluster.sync();  // a block's shared memory stays until it has been read
@@ -607,7 +627,7 @@ cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
   // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives of fp32 rows: one of
   // 128256 10.4 us, 18.0 as one block; 64 of 151936 14.8 with 4 blocks each, 22.5 with one, 25.6 with 8).
   int parts = 1;
-  while (parts < 8 && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
+  while (parts < kMaxParts && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
   return launch<T, 256>(p, parts, n_sm, stream);
 }
 
