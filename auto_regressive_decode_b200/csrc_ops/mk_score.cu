@@ -625,7 +625,7 @@ cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
   // 200 of 32000 13.0 against 10.7).
   if (p.rows > 3 * n_sm && p.vocab <= 32768) return launch<T, 128>(p, 1, n_sm, stream);
   // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives of fp32 rows: one of
-  // 128256 10.4 us, 18.0 as one block; 64 of 151936 14.8 with 4 blocks each, 22.5 with one, 25.6 with 8).
+  // 128256 9.5 us, 18.0 as one block; 64 of 151936 14.6 with 4 blocks each, 22.5 with one, 25.6 with 8).
   int parts = 1;
   while (parts < kMaxParts && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
   return launch<T, 256>(p, parts, n_sm, stream);
