@@ -95,39 +95,49 @@ __global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots
   };
   fetch(slot);  // in flight while the token finds its place
 
-  // the token's sequence: how many sequences end at or before it
-  int b = t, first = t;
+  // The token's sequence, its first token and the rows held before: a thread a sequence, all its loads at once.
+  int b = t, first = t, held;
   if (p.starts) {
-    int ends = 0;
+    __shared__ int owner[3];
     bool bad = false;
+    int found = 0;
     for (int i = threadIdx.x; i - (int)threadIdx.x < c.B; i += kThreadsA) {
-      const int lo = i < c.B ? __ldg(p.starts + i) : 0, hi = i < c.B ? __ldg(p.starts + i + 1) : 0;
+      const bool in = i < c.B;
+      const int lo = in ? __ldg(p.starts + i) : 0, hi = in ? __ldg(p.starts + i + 1) : 0, n = in ? __ldg(p.seq_lens + i) : 0;
       bad |= lo > hi || lo < 0 || hi > p.n_tokens;
-      ends += __syncthreads_count(i < c.B && hi <= t);
+      if (lo <= t && t < hi) {
+        owner[0] = i;
+        owner[1] = lo;
+        owner[2] = n;
+      }
+      found |= __syncthreads_or(lo <= t && t < hi);
     }
     if (bad) set_status(c.status, MK_ERR_RANGE, t);
-    b = ends;
-    if (b >= c.B) return;  // behind the last sequence
-    first = __ldg(p.starts + b);
-    if (t < first) return;
+    if (!found) return;  // before the first sequence or behind the last
+    b = owner[0];
+    first = owner[1];
+    held = owner[2];
+  } else {
+    held = __ldg(p.seq_lens + t);
   }
-  const int64_t row = (int64_t)__ldg(p.seq_lens + b) + (t - first);
+  const int64_t row = (int64_t)held + (t - first);
   const int pos = p.positions ? __ldg(p.positions + t) : (int)row;
-  bool ok = row >= 0 && row < c.T && pos >= 0 && pos < c.T, in_pool = true;
+  const bool ok = row >= 0 && row < c.T && pos >= 0 && pos < c.T;
+  bool in_pool = true;
   int64_t at = 0;
-  if (ok) at = c.row(p.layer, b, (int)row, &in_pool);
-  if (!ok || !in_pool) {
-    if (threadIdx.x == 0) set_status(c.status, MK_ERR_RANGE, t);
-    return;
-  }
   float cs[8], sn[8];
-  {
+  if (ok) {  // the page's entry and the rotations: neither waits for the other
     const float4* r4 = reinterpret_cast<const float4*>(p.rope + (int64_t)pos * (HD / 2) + lane * 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 f = __ldg(r4 + i);
       cs[2 * i] = f.x; sn[2 * i] = f.y; cs[2 * i + 1] = f.z; sn[2 * i + 1] = f.w;
     }
+    at = c.row(p.layer, b, (int)row, &in_pool);
+  }
+  if (!ok || !in_pool) {
+    if (threadIdx.x == 0) set_status(c.status, MK_ERR_RANGE, t);
+    return;
   }
   // Whole warps walk the rows together (the norm's sums are warp shuffles).
   const int warp_slot = blockIdx.y * kSlots + (threadIdx.x & ~31) / kLanes;
