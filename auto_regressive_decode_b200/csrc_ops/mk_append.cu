@@ -5,7 +5,7 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain
 //   out[i]     = y[i] cos a_i - y[i + hd/2] sin a_i
 //   out[i + h] = y[i + hd/2] cos a_i + y[i] sin a_i,   a_i = pos theta^(-2i/hd)
-// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 234 us, 6.5
+// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 232 us, 6.5
 // TB/s; 4100 of 48 bf16 rows 21.5 us, 4.7 TB/s (the latency of finding a token's place; 17.7 with the
 // rows in the L2 cache); one token of each of 8 sequences 2.6 us, a launch.
 // hd/16 neighbouring lanes hold a row, each 8 values of its first half and the 8
@@ -60,9 +60,10 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
 
 // Block (t, y): token t, rows y * kSlots + slot, stepping by all slots of the
 // token.  kSlots rows at once, R of them in a lane's registers before it uses
-// the first.  A token's place takes three loads that wait for each other; what
-// hides them is the number of resident blocks, hence few threads and registers a
-// block: 16000 tokens of 32 rows of 64 took 43 us with 32 slots and R = 4, 25 us with 16 and 2.
+// the first.  A token's place takes two loads that wait for each other (its sequence's numbers,
+// then its page beside its rotations; one after the other, four loads, 16000 tokens of 32 rows of 64
+// took 29 us instead of 26).  What hides them is the number of resident blocks, hence few threads
+// and registers a block: the same tokens took 43 us with 32 slots and R = 4, 25 with 16 and 2 (rows in L2).
 // Tokens of many rows want the larger block: 16384 of 120 fp32 rows of 128 245 us with 16 slots, 230 with 32
 // (at 128 registers: two blocks an SM; the compiler's own choice, 140, took 144 us instead of 101 for 6000 with norms).
 template <typename T, int HD, int kSlots, int R>
