@@ -253,7 +253,7 @@ typedef struct mk_cache mk_cache;
  * borrowed.
  */
 int mk_cache_create(const mk_cache_desc* desc, const mk_kv* kv, mk_cache** out);
-/* Waits for the device's work on the handle.  NULL is accepted. */
+/* Waits for the device's work, so not within a stream capture.  NULL is accepted. */
 int mk_cache_destroy(mk_cache* c);
 /* Synchronise `stream` and return the first error that calls recorded on the
  * device (MK_OK, MK_ERR_RANGE, MK_ERR_DEVICE_TIMEOUT); the error is cleared.

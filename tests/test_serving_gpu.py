@@ -246,3 +246,36 @@ def test_far_pages_of_a_large_pool_equal_near_ones(batch):
         del k, v
     for a, b in zip(*outs):
         assert torch.equal(a, b) and not torch.isnan(a).any()
+
+
+FIRST_CALLS = """
+import torch
+import auto_regressive_decode_b200.mk as mk
+g = torch.Generator("cuda").manual_seed(0)
+B, nq, nkv, hd, T = 40, 8, 2, 64, 400
+k, v = (torch.randn((1, B, nkv, T, hd), generator=g, device="cuda").bfloat16() for _ in range(2))
+c = mk.Cache(k, v, n_q_heads=nq, batch=B, max_ctx=T)
+x = torch.randn((B, nq + 2 * nkv, hd), generator=g, device="cuda")
+lens = torch.full((B,), 300, dtype=torch.int32, device="cuda")
+more = lens + 1
+logits, tok = torch.randn((3, 50000), generator=g, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+
+def calls():
+    q = c.append(0, x[:, nq:nq + nkv], x[:, nq + nkv:], lens, q=x[:, :nq])
+    return (q, *c.attend(0, q, more, prefix_len=200), *c.attend(0, q, more), *mk.token_logprobs(logits, tok, top_k=5))
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    inside = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(inside, calls())) and c.status() == 0
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
