@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
 // loads that wait for each other; for thousands of rows the pieces' bytes (8192 rows, 24 MB: 8 us).
 template <int HD, int W>
 __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ AttendParams p) {
-  constexpr int V = HD / 32;
+  constexpr int V = HD / 32, kEarly = 4;
   __shared__ float so[4][HD];
   __shared__ float2 sml[4];
   const CacheView& c = p.c;
@@ -603,7 +603,17 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   const float* o1 = p.own_o + (at1 - (int64_t)n0 * p.group) * HD + lane * V;
   float M = -INFINITY, L = 0.f, o[V] = {};
   for (int i0 = sub; i0 < n; i0 += 32 * W) {  // 32 pieces at a time: a lane's weight, then the weighted sum
-    const int i = i0 + lane * W;
+    const int i = i0 + lane * W, k = min(32, (n - i0 + W - 1) / W);
+    auto piece = [&](int q, float* v) {
+      const int iq = i0 + q * W;
+      const float* po = iq < n0 ? o0 + (int64_t)iq * (step * HD) : o1 + (int64_t)iq * (p.group * HD);
+      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po);
+    };
+    float early[kEarly][V];  // the first outputs come while the weights do
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q)
+      if (q < k) piece(q, early[q]);
     float2 x = make_float2(-INFINITY, 0.f);
     if (i < n) x = i < n0 ? ml0[(int64_t)i * step] : ml1[(int64_t)i * p.group];
     float m = x.x;
@@ -619,17 +629,19 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
     M = m;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] *= back;
-    const int k = min(32, (n - i0 + W - 1) / W);
-#pragma unroll 4
-    for (int q = 0; q < k; ++q) {
-      const int iq = i0 + q * W;
-      const float* po = iq < n0 ? o0 + (int64_t)iq * (step * HD) : o1 + (int64_t)iq * (p.group * HD);
-      float v[V];
-      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po);
+    auto add = [&](int q, const float* v) {
       const float wq = __shfl_sync(0xffffffffu, w, q);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = wq == 0.f ? o[e] : fmaf(v[e], wq, o[e]);
+    };
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q)
+      if (q < k) add(q, early[q]);
+#pragma unroll 4
+    for (int q = kEarly; q < k; ++q) {
+      float v[V];
+      piece(q, v);
+      add(q, v);
     }
   }
   if (W > 1) {  // the warps' parts

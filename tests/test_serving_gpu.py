@@ -275,7 +275,9 @@ assert all(torch.equal(a, b) for a, b in zip(inside, calls())) and c.status() ==
 
 
 def test_the_first_calls_of_a_process_can_be_captured():
+    import os
     import subprocess
     import sys
-    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300, cwd=root)
     assert r.returncode == 0, r.stderr[-2000:]
