@@ -21,7 +21,7 @@
 // Measured with the join, heads of 128: 32 sequences of 4000 to 4096 positions, 8 KV heads,
 // 87 us, 6.1 TB/s; 8 sequences of 40 heads over 2048 shared and up to 2048 own positions
 // 42 us, 5.2 TB/s; 512 sequences of 64 positions 42 us, 3.4 TB/s (starting and ending a
-// piece takes 2600 of its 5500 clocks); one sequence over 1024 7.9 us, two launches' latency.
+// piece takes 2600 of its 5500 clocks); one sequence over 1024 7.4 us, two launches' latency.
 //
 // Up to 8 rows (NARROW) are the N of the products, S^T = K Q^T and O^T = V^T P^T;
 // more are their M, 16 at a time.  As M, 8 rows would take twice the products and
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
   grid_wait();
 }
 
-// Joins the pieces of every row: W warps a row take them in turn.  Bound: the latency of four
-// loads that wait for each other; for thousands of rows the pieces' bytes (8192 rows, 24 MB: 8 us).
+// Joins the pieces of every row: W warps a row take them in turn.  Bound: the latency of three
+// loads that wait for each other (four, with the first outputs behind their weights: 0.5 us more); for thousands of rows the pieces' bytes (8192 rows, 24 MB: 8 us).
 template <int HD, int W>
 __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ AttendParams p) {
   constexpr int V = HD / 32, kEarly = 4;
