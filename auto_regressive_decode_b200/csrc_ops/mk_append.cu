@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots
       }
     }
   };
+  grid_wait();  // launched while the kernel ahead is under way; nothing of its is read before
+  grid_launch_next();
   fetch(slot);  // in flight while the token finds its place
 
   // The token's sequence, its first token and the rows held before: a thread a sequence, all its loads at once.
@@ -221,8 +223,16 @@ cudaError_t append(const mk_cache& c, int layer, const mk_append_args& a, cudaSt
   const int rows = (most + (int)grid.y - 1) / (int)grid.y;  // a lane's
   const auto kernel = c.d.head_dim == 128 ? (es == 2 ? pick<uint16_t, 128>(slots, rows) : pick<float, 128>(slots, rows))
                                           : (es == 2 ? pick<uint16_t, 64>(slots, rows) : pick<float, 64>(slots, rows));
-  kernel<<<grid, slots * (c.d.head_dim / 16), 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(slots * (c.d.head_dim / 16));
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace mk
