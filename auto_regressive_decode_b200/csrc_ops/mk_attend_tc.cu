@@ -67,8 +67,10 @@ struct TcLayout {
 };
 
 struct TcCtl {
-  unsigned long long full[8], empty[8];
-  unsigned long long q_full, tail, s_full[2], p_half[2], p_full[2], o_done[2];  // [stream]
+  // tail[slot]: what lies behind the prefix in the slot's V tile is cleared.  One a slot, so that its phase cannot
+  // run ahead of those who wait for it: the slot is filled again only after its tile has been read.
+  unsigned long long full[8], empty[8], tail[8];
+  unsigned long long q_full, s_full[2], p_half[2], p_full[2], o_done[2];  // [stream]
   uint32_t tmem;
   int dead, max_len;
 };
@@ -130,9 +132,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(smem_addr(&ctl->full[s]), 1);
       mbar_init(smem_addr(&ctl->empty[s]), 2);
+      mbar_init(smem_addr(&ctl->tail[s]), 1);
     }
     mbar_init(smem_addr(&ctl->q_full), kSoftmaxThreads);
-    mbar_init(smem_addr(&ctl->tail), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&ctl->s_full[s]), 1);
       mbar_init(smem_addr(&ctl->p_half[s]), kSoftmaxThreads / 2);
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&ctl->tail));
+          if (lane == 0) mbar_arrive(smem_addr(&ctl->tail[slot]));
         }
         if (++slot == S::kSlots) slot = 0, phase ^= 1;
       }
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t q_desc = smem_desc(base + S::kQ, 16, 1024), k_desc = smem_desc(base, 16, 1024),
                    v_desc = smem_desc(base, kTcTile * 128, 1024);
     uint32_t at = 0;  // tiles that passed through the ring in earlier pieces
-    uint32_t q_phase = 0, tail_phase = 0, p_phase = 0;
+    uint32_t q_phase = 0, tail_phase = 0 /* a bit a slot */, p_phase = 0;
     const uint32_t s_full = smem_addr(&ctl->s_full[s]), p_half = smem_addr(&ctl->p_half[s]), p_full = smem_addr(&ctl->p_full[s]), o_done = smem_addr(&ctl->o_done[s]);
     const uint32_t s_col = tmem + kS + s * 128, o_col = tmem + kO + s * 128;
     // The streams' warps take turns.  A product is issued as the matrix unit takes it (65 to
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int t = a.pair ? i : 2 * i + s;
           const uint32_t place = at + v_place(a.pair, t, a.n), slot = place % S::kSlots;
           mbar_wait(smem_addr(&ctl->full[slot]), place / S::kSlots & 1, dead);
-          if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail), tail_phase, dead);
+          if (a.t0 + t == whole_tiles) mbar_wait(smem_addr(&ctl->tail[slot]), tail_phase >> slot & 1, dead);
           v = v_desc + slot * (S::kSlotBytes >> 4);
           if (i + 1 < n) k = k_tile(i + 1);
           mbar_wait(p_half, p_phase, dead);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         pass_turn();
       }
-      if (a.t0 + a.n > whole_tiles) tail_phase ^= 1;
+      if (a.t0 + a.n > whole_tiles) tail_phase ^= 1u << (at + 2 * a.n - 1) % S::kSlots;  // the piece's last tile was the cleared one
       at += 2 * a.n;
     }
     if (s == 0) take_turn();  // the last one passed
