@@ -672,7 +672,8 @@ __global__ void __launch_bounds__(128) attend_join(const __grid_constant__ Atten
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * HD + lane * V);
 #pragma unroll
   for (int e = 0; e < V; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+  // by the sum: maxima drop NaN, so that M alone cannot tell a row of NaN scores from one without positions
+  if (p.lse && lane == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
 }
 
 // Workspace: schedule, then the pieces of the prefix and of the own positions.

@@ -318,7 +318,8 @@ int mk_cache_append(mk_cache* c, int layer, const mk_append_args* args, void* st
  * Scores, softmax sums and output sums are fp32; the probabilities are rounded
  * to bf16 as operands of the second product.  Rows that no sequence attends may
  * hold anything.  A NaN or infinite value in a shared row also reaches sequences
- * that end before it (0 times it is NaN); a key does not.
+ * that end before it (0 times it is NaN); a key does not.  A row with a score
+ * of NaN or +infinity has nothing but NaN in out and lse.
  */
 int mk_cache_attend(mk_cache* c, int layer, const void* q, const int32_t* seq_lens, int prefix_len, float scale,
                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
