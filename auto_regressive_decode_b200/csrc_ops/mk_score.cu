@@ -1,10 +1,11 @@
 // Log probabilities of given tokens, entropy and the most likely alternatives.
 //
-// One pass over a row of logits x.  Every thread keeps a reference m near its
-// maximum and, in units of log2 (d = (x - m) log2 e), z = sum 2^d and
-// s = sum 2^d d; the threads' (m, z, s) move to the largest m at the end:
+// One pass over a row of logits x.  Every warp keeps its maximum m so far, every
+// thread, in units of log2 (d = (x - m) log2 e), z = sum 2^d and s = sum 2^d d;
+// the warps' (m, z, s) move to the row's maximum at the end:
 //   logprob(t) = x_t - m - ln z,   entropy = ln z - ln 2 * s / z
-// (terms of one sign but for the few above the reference: nothing cancels).
+// With the true maximum z is 1 at least and s 0 at most: nothing cancels, and a token that is all but
+// certain keeps its small log probability (references up to 16 below the maximum left 1e-6 of both logarithms).
 //
 // Alternatives: a key packs the order-preserving map of the logit over the
 // inverted index, so that the largest key is the largest logit, of the lowest
@@ -54,6 +55,12 @@ struct ScoreParams {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Largest of the warp's 32 values, none of them NaN.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -221,8 +228,8 @@ __device__ __forceinline__ float given_logit(const ScoreParams& p, const T* x, i
   return t >= 0 && t < p.vocab ? Vec<T>::one(x[t]) : NAN;
 }
 
-// A thread's sums.  d = x log2 e - c is one fma, c = m log2 e rounded; what the
-// rounding left (res) is put right when the sums move to another reference.
+// A thread's sums, m the maximum of its warp so far.  d = x log2 e - c is one fma, c = m log2 e rounded;
+// what the rounding left (res) is put right when the sums move to another maximum.
 struct Acc {
   float m = -INFINITY, c = 0.f, res = 0.f, z = 0.f, s = 0.f;
   bool huge = false;  // m log2 e overflows, or its rounding is no small part of a power of two
@@ -233,18 +240,18 @@ struct Acc {
     s = f > 0.f ? f * (s + z * dm) : 0.f;
     z *= f;
   }
-  // A new reference; the next one comes when a logit is kSlack above it: 2^d
-  // and its sums stay far inside fp32, so that few chunks move the sums.
-  static constexpr float kSlack = 16.f;
-  __device__ __noinline__ void lift(float top, float& lifted) {
+  // The warp's maximum has grown: `top` is this thread's largest logit, above it in some thread.
+  __device__ __forceinline__ void lift(float top) {
     const float m0 = m, res0 = res;
+    top = warp_max(top);
     m = top;
     huge = fabsf(top) > 1e6f;
     c = huge ? 0.f : top * kLog2e;
     res = huge ? 0.f : fmaf(top, kLog2e, -c);
     move(m0 == -INFINITY ? 0.f : (m0 - top) * kLog2e - res0 + res);
-    lifted = top + kSlack;
   }
+  // d, bounded where 2^d is 0: 0 * -infinity is NaN
+  __device__ __forceinline__ float bounded(float x) const { return max_nan(huge ? (x - m) * kLog2e : fmaf(x, kLog2e, -c), -150.f); }
   __device__ __forceinline__ Sum sum() {
     move(-res);
     return Sum{m, z, s};
@@ -253,9 +260,7 @@ struct Acc {
 
 // Sum of the 32 lanes, in every lane.
 __device__ __forceinline__ Sum warp_join(Sum a) {
-  float m = a.m;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float m = warp_max(a.m);
   Sum r{m, 0.f, 0.f};
   if (a.z != 0.f) {  // else nothing but -infinity (a NaN sum is passed on)
     const float dm = (a.m - (m == -INFINITY ? 0.f : m)) * kLog2e, f = ex2(dm);
@@ -332,7 +337,6 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
   for (int row = row0; row < p.rows; row += row_step) {
     const Part<T> r(p, row, part, parts);
     Acc acc;
-    float lifted = -INFINITY;  // what the next reference has to exceed
     // The thread's largest chunk maximum and the two next ones, each the first of equal ones; their chunks (as first
     // vectors; -1: none, or the row's partial vectors, whose keys are already among the warp's).
     float most = -INFINITY, second = -INFINITY, third = -INFINITY;
@@ -380,9 +384,10 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       const bool in = lane < VEC ? r.skew && i < VEC - r.skew && i < p.vocab : lane < 2 * VEC && i < p.vocab;
       const float f = in ? Vec<T>::one(r.x[i]) : -INFINITY;
       most = fmaxf(f, -INFINITY);
-      if (most > -INFINITY) acc.lift(most, lifted);
-      acc.z = f == -INFINITY ? 0.f : (fabsf(f) < INFINITY ? ex2(acc.res) : NAN);
-      acc.s = acc.z * acc.res;
+      if (__any_sync(0xffffffffu, most > -INFINITY)) acc.lift(most);
+      const float d = acc.bounded(f);
+      acc.z = ex2(d);
+      acc.s = acc.z * d;
       if (k > 0) push(f > -INFINITY ? make_key(f, i) : 0);
     }
 
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
         most = first ? top : most;
         where = first ? v0 : where;
       }
-      if (top > lifted) acc.lift(top, lifted);
+      if (__any_sync(0xffffffffu, top > acc.m)) acc.lift(top);
       F2 z2 = pack2(0.f, 0.f), s2 = z2;
       const F2 back = pack2(-acc.c, -acc.c), scale = pack2(kLog2e, kLog2e);
 #pragma unroll
@@ -435,8 +440,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       unpack2(s2, s0, s1);
       float z = z0 + z1, s = s0 + s1;
       if (!(s == s) || acc.huge) {
-        // 0 * -infinity (masked logits), a real NaN, or a reference too large for the fma:
-        // again, with the exponent bounded where 2^d is 0
+        // 0 * -infinity (masked logits), a real NaN, or a maximum too large for the fma: again, bounded
         z = s = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
           Vec<T>::get(raw[u], f);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
-            const float d = max_nan(acc.huge ? (f[i] - acc.m) * kLog2e : fmaf(f[i], kLog2e, -acc.c), -150.f), e = ex2(d);
+            const float d = acc.bounded(f[i]), e = ex2(d);
             z += e;
             s = fmaf(e, d, s);
           }
@@ -573,9 +577,11 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       cluster.sync();  // a block's shared memory stays until it has been read
     }
     if (part == 0) {
-      const Sum q = sh.sum;
+      Sum q = sh.sum;
+      if (q.z < 1.f) q.z = 1.f;  // less, or s above 0, is rounding: no log probability above 0, no entropy below
+      if (q.s > 0.f) q.s = 0.f;
       const float lnz = logf(q.z);
-      const bool none = !(q.z > 0.f) || isinf(q.m) || *dead;  // NaN, infinities, nothing allowed (or a copy that never came)
+      const bool none = !(q.z == q.z) || isinf(q.m) || *dead;  // NaN, infinities, nothing allowed (or a copy that never came)
       if (tid == 0) {
         if (parts > 1) given = sh.given;
         p.logprob[row] = none ? NAN : given - q.m - lnz;
