@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
     compute_bar<NT>();
     if (warp == 0) {
       a = warp_join(lane < S::kWarps ? sh.part[lane] : Sum{-INFINITY, 0.f, 0.f});
+      if (*dead) a.z = NAN;  // a copy never came: the block's share, and with it the row, has no scores
       if (lane == 0) sh.sum = a;
     }
     int n = 0, got = 0;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 256 ? 3 : 6) score_kernel(const
       if (q.z < 1.f) q.z = 1.f;  // less, or s above 0, is rounding: no log probability above 0, no entropy below
       if (q.s > 0.f) q.s = 0.f;
       const float lnz = logf(q.z);
-      const bool none = !(q.z == q.z) || isinf(q.m) || *dead;  // NaN, infinities, nothing allowed (or a copy that never came)
+      const bool none = !(q.z == q.z) || isinf(q.m);  // NaN (a copy that never came, too), infinities, nothing allowed
       if (tid == 0) {
         if (parts > 1) given = sh.given;
         p.logprob[row] = none ? NAN : given - q.m - lnz;
