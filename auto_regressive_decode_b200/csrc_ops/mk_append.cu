@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots
       }
     }
   };
-  grid_wait();  // launched while the kernel ahead is under way; nothing of its is read before
+  // Launched while the kernel ahead is under way; nothing of its is read before.  Nor is anything that it may write read as
+  // constant (__ldg): only the rotations are.
+  grid_wait();
   grid_launch_next();
   fetch(slot);  // in flight while the token finds its place
 
@@ -102,29 +104,28 @@ __global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots
   int b = t, first = t, held;
   if (p.starts) {
     __shared__ int owner[3];
-    bool bad = false;
-    int found = 0;
-    for (int i = threadIdx.x; i - (int)threadIdx.x < c.B; i += kThreadsA) {
-      const bool in = i < c.B;
-      const int lo = in ? __ldg(p.starts + i) : 0, hi = in ? __ldg(p.starts + i + 1) : 0, n = in ? __ldg(p.seq_lens + i) : 0;
+    bool bad = false, mine = false;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < c.B; i += kThreadsA) {
+      const int lo = p.starts[i], hi = p.starts[i + 1], n = p.seq_lens[i];
       bad |= lo > hi || lo < 0 || hi > p.n_tokens;
       if (lo <= t && t < hi) {
         owner[0] = i;
         owner[1] = lo;
         owner[2] = n;
+        mine = true;
       }
-      found |= __syncthreads_or(lo <= t && t < hi);
     }
     if (bad) set_status(c.status, MK_ERR_RANGE, t);
-    if (!found) return;  // before the first sequence or behind the last
+    if (!__syncthreads_or(mine)) return;  // before the first sequence or behind the last
     b = owner[0];
     first = owner[1];
     held = owner[2];
   } else {
-    held = __ldg(p.seq_lens + t);
+    held = p.seq_lens[t];
   }
   const int64_t row = (int64_t)held + (t - first);
-  const int pos = p.positions ? __ldg(p.positions + t) : (int)row;
+  const int pos = p.positions ? p.positions[t] : (int)row;
   const bool ok = row >= 0 && row < c.T && pos >= 0 && pos < c.T;
   bool in_pool = true;
   int64_t at = 0;
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(kSlots * HD / 16, kSlots == 32 ? 512 / (kSlots
         if (gain && h < nh) {
           const float inv = rsqrtf(ss * (1.0f / HD) + p.eps);  // off by 2^-22 at most: a root and a division took 5 to 10 % of the call
           Vec8<uint16_t> ga, gb;
-          ga.a = __ldg(reinterpret_cast<const uint4*>(gain + lane * 8));
-          gb.a = __ldg(reinterpret_cast<const uint4*>(gain + HD / 2 + lane * 8));
+          ga.a = *reinterpret_cast<const uint4*>(gain + lane * 8);
+          gb.a = *reinterpret_cast<const uint4*>(gain + HD / 2 + lane * 8);
           float g[8];
           ga.get(g);
 #pragma unroll

@@ -197,11 +197,12 @@ __global__ void __launch_bounds__(kAttThreads, Layout<HD, NARROW>::kBlocksPerSm)
     prefetch_map(&vmap);
   }
   // Nothing is read or written before the kernel ahead is done (after attend_prefix_tc: the one ahead of
-  // that, whose own wait precedes this launch; their workspaces are apart).
-  if (!p.tc) grid_wait();
+  // that, whose own wait precedes this launch; their workspaces are apart.  The fence: no line of the first cache from before).
+  if (p.tc) fence_gpu();
+  else grid_wait();
   grid_launch_next();
   for (int b = tid; b < c.B; b += kAttThreads) {
-    const int n = __ldg(p.seq_lens + b), m = n < 0 ? 0 : min(n, c.T);
+    const int n = p.seq_lens[b], m = n < 0 ? 0 : min(n, c.T);
     if (n != m && blockIdx.x == 0) set_status(c.status, MK_ERR_RANGE, b);
     lens[b] = m;
   }

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   grid_wait();  // nothing is read or written before the kernel ahead is done
   grid_launch_next();
   int longest = 0;
-  for (int b = tid; b < cv.B; b += kTcThreads) longest = max(longest, min(__ldg(p.seq_lens + b), cv.T));
+  for (int b = tid; b < cv.B; b += kTcThreads) longest = max(longest, min(p.seq_lens[b], cv.T));
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) atomicMax(&ctl->max_len, longest);
   tc_fence_before();
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row = (a.pair ? s * kTcRows : 0) + r;
       const bool valid = row < a.rows;
       const int b = (a.row0 + row) / p.group;
-      const int lim = valid ? min(__ldg(p.seq_lens + b), prefix_end) : 0;
+      const int lim = valid ? min(p.seq_lens[b], prefix_end) : 0;
       if (a.pair || s == 0) {  // the query tile, a thread a 16-byte chunk of every kStep-th row, swizzled as TMA would
         constexpr int kChunks = HD / 8, kStep = 256 / kChunks;
         const int ch = tid % kChunks, first = tid % 256 / kChunks, row0 = a.pair ? s * kTcRows : 0;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < kTcRows / kStep; ++i) {
           x[i] = make_uint4(0, 0, 0, 0);
           if (row0 + first + i * kStep < a.rows)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)qb * cv.nq + a.kvh * p.group + qj) * HD) + ch);
+            x[i] = reinterpret_cast<const uint4*>(p.q + ((int64_t)qb * cv.nq + a.kvh * p.group + qj) * HD)[ch];
           qb += step_b;
           qj += step_j;
           if (qj >= p.group) qj -= p.group, ++qb;

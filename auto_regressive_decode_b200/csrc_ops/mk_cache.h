@@ -29,7 +29,7 @@ struct CacheView {
   // A page outside the pool is recorded and read as page 0 (*ok = false).
   __device__ __forceinline__ int64_t row(int layer, int b, int pos, bool* ok) const {
     if (bt) {
-      int pg = __ldg(bt + (int64_t)b * bt_stride + pos / page);
+      int pg = bt[(int64_t)b * bt_stride + pos / page];
       *ok = pg >= 0 && pg < n_pages;
       if (!*ok) pg = 0;
       return ((int64_t)layer * n_pages + pg) * nkv * page + pos % page;

@@ -99,10 +99,13 @@ __device__ __forceinline__ void bulk_stores_read() {
 __device__ __forceinline__ void bulk_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---- programmatic dependent launch ---------------------------------------------------
-// Wait until every grid that this one depends on has finished and its writes are visible.
+// Wait until every grid that this one depends on has finished and its writes are visible.  What such a grid may write is
+// not read as constant (__ldg), although this grid does not write it: the compiler may move that load above the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Let the next grid of the stream begin its part before grid_wait().
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 // ---- mma.sync fragments -----------------------------------------------------------
 __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
