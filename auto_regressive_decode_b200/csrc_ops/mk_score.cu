@@ -677,8 +677,10 @@ extern "C" int mk_decode_greedy_scored(mk_handle* h, const mk_model_desc* desc, 
       desc->vocab <= 0 || top_k < 0 ||
       (n_steps > 0 && (!out_tokens || !logits || !out_logprob || (top_k > 0 && (!out_top_ids || !out_top_logprobs)))))
     return MK_ERR_INVALID_ARG;
-  if (mk_state_bytes(h, MK_STATE_HIDDEN) != sizeof(float) * (2 * (size_t)desc->n_layers + 1) * desc->batch * desc->hidden)
-    return MK_ERR_INVALID_ARG;  // not the handle's
+  // The handle's own description is its first member (csrc/mk_api.cu): the buffers are of its sizes.
+  const mk_model_desc& own = *reinterpret_cast<const mk_model_desc*>(h);
+  if (own.n_layers != desc->n_layers || own.batch != desc->batch || own.hidden != desc->hidden || own.vocab != desc->vocab)
+    return MK_ERR_INVALID_ARG;
   if (top_k > mk::kMaxTop) return MK_ERR_UNSUPPORTED;
   cudaStream_t s = (cudaStream_t)stream;
   const int B = desc->batch;

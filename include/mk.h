@@ -348,7 +348,7 @@ int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_r
 /*
  * mk_decode_greedy with the scores of every picked token, mk_token_logprobs of
  * each step's logits.  `desc` is the one the handle was created with
- * (MK_ERR_INVALID_ARG where layers, batch or width differ).
+ * (MK_ERR_INVALID_ARG where layers, batch, width or vocabulary differ).
  *   out_lens   device int32[batch]: the lengths after the loop (also its
  *              working state; not the array seq_lens)
  *   logits     device fp32[batch][vocab]: the last step's logits afterwards

@@ -1,0 +1,41 @@
+"""What mk_decode_greedy_scored refuses of its description, whose sizes the buffers have to be of."""
+import numpy as np
+import pytest
+import torch
+
+import fixtures as fx
+from fixtures.device import device_caches, device_model
+
+pytestmark = pytest.mark.gpu
+
+
+def decoder(**kw):
+    import auto_regressive_decode_b200.mk as mk
+    cfg = fx.CONFIGS["tiny"].replace(batch=4, ffn_dim=704, ctx=0, ctx_lo=5, ctx_hi=100, **kw)
+    S0 = fx.context_lengths(cfg)
+    kc, vc = device_caches(cfg, S0)
+    tok = torch.from_numpy(fx.tokens(cfg)[0].copy()).cuda()
+    return cfg, mk.Decoder(cfg, device_model(cfg), kc, vc), tok, torch.from_numpy(S0.astype(np.int32)).cuda()
+
+
+def test_descriptions_that_differ_from_the_handles():
+    """Another vocabulary, and sizes whose product of layers, batch and width is the handle's."""
+    import auto_regressive_decode_b200.mk as mk
+    cfg, dec, tok, lens = decoder()
+    right = dec.desc
+    others = [{"vocab": cfg.vocab * 2}, {"vocab": cfg.vocab // 2}, {"batch": 2, "hidden": 2 * cfg.hidden}, {"batch": 8, "hidden": cfg.hidden // 2}]
+    picks = torch.full((3, 8), -5, dtype=torch.int32, device="cuda")
+    logits = torch.full((8, 2 * cfg.vocab), 3.0, device="cuda")       # large enough for each of them
+    for kw in others:
+        d = mk.mk_model_desc.from_buffer_copy(right)
+        for name, value in kw.items():
+            setattr(d, name, value)
+        dec.desc = d
+        with pytest.raises(mk.MkError) as e:
+            dec.greedy_scored(3, tok, lens, picks, logits=logits)
+        assert e.value.code == mk.MK_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (picks == -5).all() and (logits == 3.0).all()
+    dec.desc = right
+    dec.greedy_scored(3, tok, lens, picks)
+    assert dec.status() == mk.MK_OK and (picks.view(-1)[:3 * cfg.batch] >= 0).all()
