@@ -272,20 +272,29 @@ class Decoder:
     def greedy_scored(self, n_steps, tokens, seq_lens, out_tokens, top_k=0, logits=None, stream=None):
         """greedy() with the scores of every picked token (asynchronous): (logprob [n][B], entropy [n][B], top ids
         int32 [n][B][top_k], their log probabilities, lengths after the loop int32 [B]); see token_logprobs.  logits:
-        float32 [B][vocab] working buffer, the last step's logits afterwards."""
+        float32 [B][vocab] working buffer, the last step's logits afterwards.  Everything is on the decoder's device, the
+        stream too; that need not be the current device."""
         torch = self.torch
-        st = stream or torch.cuda.current_stream()
+        device = self._keep[1].device
         B, V = self.cfg.batch, self.cfg.vocab
-        with torch.cuda.stream(st):
-            lg = torch.empty((B, V), dtype=torch.float32, device="cuda") if logits is None else logits
-            lens = torch.empty((B,), dtype=torch.int32, device="cuda")
-            logprob, entropy = torch.empty((2, n_steps, B), dtype=torch.float32, device="cuda")
-            ids = torch.empty((n_steps, B, top_k), dtype=torch.int32, device="cuda")
-            tops = torch.empty((n_steps, B, top_k), dtype=torch.float32, device="cuda")
-        check(mk_decode_greedy_scored(self.h, ctypes.byref(self.desc), n_steps, tokens.data_ptr(), seq_lens.data_ptr(),
-                                      st.cuda_stream, out_tokens.data_ptr(), lens.data_ptr(), lg.data_ptr(),
-                                      logprob.data_ptr(), entropy.data_ptr(), top_k, ids.data_ptr(), tops.data_ptr()),
-              "mk_decode_greedy_scored")
+        if n_steps < 0 or top_k < 0:
+            _refuse("greedy_scored: n_steps and top_k are 0 at least")
+        _require("greedy_scored", "tokens", tokens, torch.int32, B, device)
+        _require("greedy_scored", "seq_lens", seq_lens, torch.int32, B, device)
+        _require("greedy_scored", "out_tokens", out_tokens, torch.int32, n_steps * B, device)
+        if logits is not None:
+            _require("greedy_scored", "logits", logits, torch.float32, B * V, device)
+        st = stream or torch.cuda.current_stream(device)
+        with _on_stream(st, device):
+            lg = torch.empty((B, V), dtype=torch.float32, device=device) if logits is None else logits
+            lens = torch.empty((B,), dtype=torch.int32, device=device)
+            logprob, entropy = torch.empty((2, n_steps, B), dtype=torch.float32, device=device)
+            ids = torch.empty((n_steps, B, top_k), dtype=torch.int32, device=device)
+            tops = torch.empty((n_steps, B, top_k), dtype=torch.float32, device=device)
+            check(mk_decode_greedy_scored(self.h, ctypes.byref(self.desc), n_steps, tokens.data_ptr(), seq_lens.data_ptr(),
+                                          st.cuda_stream, out_tokens.data_ptr(), lens.data_ptr(), lg.data_ptr(),
+                                          logprob.data_ptr(), entropy.data_ptr(), top_k, ids.data_ptr(), tops.data_ptr()),
+                  "mk_decode_greedy_scored")
         return logprob, entropy, ids, tops, lens
 
     def cache(self):
@@ -359,6 +368,13 @@ def _calls():
 
 def _refuse(what):
     raise MkError(MK_ERR_INVALID_ARG, what)
+
+
+def _require(op, name, t, dtype, least, device):
+    """Refuse what is no contiguous tensor of `dtype` on `device` with `least` elements or more."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous() and t.numel() >= least):
+        _refuse(f"{op}: {name}: a contiguous {dtype} tensor of {least} elements on {device} is wanted")
 
 
 def _on_stream(stream, device):

@@ -39,3 +39,38 @@ def test_descriptions_that_differ_from_the_handles():
     dec.desc = right
     dec.greedy_scored(3, tok, lens, picks)
     assert dec.status() == mk.MK_OK and (picks.view(-1)[:3 * cfg.batch] >= 0).all()
+
+
+@pytest.mark.parametrize("bad", ["tokens type", "tokens length", "tokens host", "lens type", "lens strides", "picks type", "picks length",
+                                 "logits type", "logits length", "logits none", "steps", "top_k"])
+def test_wrong_tensors(bad):
+    import auto_regressive_decode_b200.mk as mk
+    cfg, dec, tok, lens = decoder()
+    B, V = cfg.batch, cfg.vocab
+    picks = torch.full((2, B), -5, dtype=torch.int32, device="cuda")
+    a = dict(n_steps=2, tokens=tok, seq_lens=lens, out_tokens=picks, top_k=3, logits=torch.full((B, V), 3.0, device="cuda"))
+    a.update({"tokens type": {"tokens": tok.long()}, "tokens length": {"tokens": tok[:3]}, "tokens host": {"tokens": tok.cpu()},
+              "lens type": {"seq_lens": lens.float()}, "lens strides": {"seq_lens": lens.repeat_interleave(2)[::2]},
+              "picks type": {"out_tokens": picks.long()}, "picks length": {"out_tokens": picks[:1]},
+              "logits type": {"logits": a["logits"].bfloat16()}, "logits length": {"logits": a["logits"][1:]},
+              "logits none": {"logits": 5}, "steps": {"n_steps": -1}, "top_k": {"top_k": -1}}[bad])
+    with pytest.raises(mk.MkError) as e:
+        dec.greedy_scored(**a)
+    assert e.value.code == mk.MK_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (picks == -5).all() and dec.status() == mk.MK_OK
+
+
+def test_larger_buffers_and_a_stream_of_its_own():
+    """Room for more steps than are run is fine, and the results are those of the current stream's call."""
+    cfg, dec, tok, lens = decoder()
+    B = cfg.batch
+    a, b = (torch.full((5, B), -5, dtype=torch.int32, device="cuda") for _ in range(2))
+    first = dec.greedy_scored(3, tok, lens, a, top_k=2)
+    _, dec, _, _ = decoder()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    second = dec.greedy_scored(3, tok, lens, b, top_k=2, stream=st)
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and (a[3:] == -5).all() and all(torch.equal(x, y) for x, y in zip(first, second))
