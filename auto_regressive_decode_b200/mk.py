@@ -298,7 +298,7 @@ class Decoder:
         return logprob, entropy, ids, tops, lens
 
     def cache(self):
-        """A Cache of this decoder's KV cache: rows appended through it are the ones its steps attend over."""
+        """A new Cache of this decoder's KV cache: rows appended through it are the ones its steps attend over."""
         c, (_, k, v, table) = self.cfg, self._keep
         return Cache(k, v, n_q_heads=c.n_q_heads, batch=c.batch, max_ctx=c.max_ctx, block_table=table,
                      page_size=0 if table is None else k.shape[3], rope_theta=c.rope_theta, rms_eps=c.rms_eps)
@@ -384,8 +384,24 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
+_dropped = []  # handles of caches that are gone: destroying them waits for the device, which would end a stream capture
+
+
+def _destroy_dropped():
+    while _dropped:
+        try:
+            h = _dropped.pop()
+        except IndexError:  # another thread took the last one
+            return
+        mk_cache_destroy(h)
+
+
 class Cache:
     """Owns one mk_cache: the append and attend operators on a KV cache.
+
+    Make it outside a stream capture and keep it as long as a graph captured from its calls is replayed.  Destroying a
+    handle waits for the device, so a Cache that is dropped leaves its handle to the next one that is made or closed, and close()
+    within a capture does the same.
 
     k, v: device bf16 [L][B][n_kv][max_ctx][hd], or with block_table (device int32
     [B][ceil(max_ctx/page_size)]) page pools [L][n_pages][n_kv][page_size][hd]; page_size a multiple of 16.
@@ -398,6 +414,8 @@ class Cache:
         if not (k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.dim() == 5 and k.is_cuda and
                 v.device == k.device and k.is_contiguous() and v.is_contiguous()):
             _refuse("Cache: k and v are contiguous bf16 device tensors of one shape [.][.][.][.][.]")
+        if torch.cuda.is_current_stream_capturing():
+            _refuse("Cache: a handle is made outside a stream capture")
         L, n, nkv, rows, hd = k.shape
         self.device = k.device
         if block_table is None:
@@ -415,6 +433,7 @@ class Cache:
         self._keep = (k, v, block_table)
         desc = mk_cache_desc(L, batch, n_q_heads, nkv, hd, max_ctx, rms_eps, rope_theta)
         h = _P()
+        _destroy_dropped()
         with torch.cuda.device(self.device):
             check(mk_cache_create(ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(h)), "mk_cache_create")
         self.h = h.value
@@ -445,13 +464,18 @@ class Cache:
         return mk_cache_get_status(self.h, (stream or self.torch.cuda.current_stream(self.device)).cuda_stream)
 
     def close(self):
-        if getattr(self, "h", None):
-            mk_cache_destroy(self.h)
-            self.h = 0
+        self._drop()
+        if _dropped and not self.torch.cuda.is_current_stream_capturing():
+            _destroy_dropped()
+
+    def _drop(self):
+        h, self.h = getattr(self, "h", 0), 0
+        if h:
+            _dropped.append(h)
 
     def __del__(self):
         try:
-            self.close()
+            self._drop()
         except Exception:
             pass
 

@@ -235,7 +235,8 @@ int mk_decode_step_noalloc(const mk_model_desc* desc, const mk_weights* weights,
  * restore the current one.  The calls only read it, so calls on
  * several streams may overlap as far as their buffers allow: an attend reads
  * what an earlier append of the same stream wrote, and overlapping attends
- * need a workspace each.
+ * need a workspace each.  A captured call reads the handle's table and the
+ * buffers that it was given at every replay: they have to outlive the graph.
  */
 typedef struct mk_cache_desc {
   int32_t n_layers, batch, n_q_heads, n_kv_heads, head_dim, max_ctx;
