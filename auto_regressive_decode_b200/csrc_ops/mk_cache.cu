@@ -62,8 +62,10 @@ __global__ void rope_table(float2* out, int T, int half, double theta) {
   }
 }
 
-// Device memory of the handles, from a pool of the library that keeps what is
-// freed: cudaMalloc and cudaFree take milliseconds next to live work.
+// Device memory of the handles, from a pool of the library that keeps some of what is
+// freed: cudaMalloc and cudaFree take milliseconds next to live work.  More goes back
+// to the device when a handle is destroyed (a table of 131072 positions of 128 is 64 MB).
+constexpr uint64_t kKeptBytes = 64ull << 20;
 cudaError_t pool_of(int dev, cudaMemPool_t* out) {
   static std::mutex lock;
   static cudaMemPool_t pools[64];
@@ -77,7 +79,7 @@ cudaError_t pool_of(int dev, cudaMemPool_t* out) {
     cudaMemPool_t p;
     cudaError_t e = cudaMemPoolCreate(&p, &props);
     if (e != cudaSuccess) return e;
-    uint64_t keep = UINT64_MAX;
+    uint64_t keep = kKeptBytes;
     e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
     if (e != cudaSuccess) {
       cudaMemPoolDestroy(p);
@@ -215,6 +217,7 @@ extern "C" int mk_cache_destroy(mk_cache* c) {
     mk::OnDevice here(c->device);
     e = cudaDeviceSynchronize();  // calls on any stream may still read the table
     if (e == cudaSuccess) e = cudaFreeAsync(c->region, cudaStreamPerThread);  // else it stays: better lost than read after
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamPerThread);     // what the pool holds above its limit is released
   }
   delete c;
   return mk::launched(e);

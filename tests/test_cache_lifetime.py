@@ -88,3 +88,38 @@ def test_captures_survive(how):
     more = make()
     assert not mk._dropped
     assert torch.equal(more.attend(0, q, lens)[0], want[0])
+
+
+@pytest.mark.gpu
+def test_memory_of_closed_handles_goes_back():
+    """Tables of 512 MB in all; 64 MB may stay with the library, and the driver's own blocks are of some MB."""
+    T = 1 << 18
+    k = torch.zeros((1, 1, 1, T, 128), dtype=torch.bfloat16, device="cuda")
+    table = 8 * T * 64
+
+    def make():
+        return mk.Cache(k, k, n_q_heads=1, batch=1, max_ctx=T)
+    make().close()
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    handles = [make() for _ in range(4)]
+    torch.cuda.synchronize()
+    held = before - torch.cuda.mem_get_info()[0]
+    assert held >= 4 * table - (64 << 20)
+    for h in handles:
+        h.close()
+    torch.cuda.synchronize()
+    assert before - torch.cuda.mem_get_info()[0] <= (64 << 20) + (32 << 20)
+
+
+@pytest.mark.gpu
+def test_handles_of_many_sizes_come_and_go():
+    k = torch.randn((1, 1, 1, 1 << 15, 64), device="cuda").bfloat16()
+    q, n = torch.randn((1, 1, 64), device="cuda").bfloat16(), torch.ones(1, dtype=torch.int32, device="cuda")
+    for i in range(40):
+        T = 1 + (i * 7919) % (1 << 15)
+        part = k.view(-1)[:T * 64].view(1, 1, 1, T, 64)
+        c = mk.Cache(part, part, n_q_heads=1, batch=1, max_ctx=T)
+        assert torch.equal(c.attend(0, q, n)[0], part[0, :, :, 0])
+        if i % 3:
+            c.close()
