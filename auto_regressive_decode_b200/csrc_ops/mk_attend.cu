@@ -783,7 +783,7 @@ cudaError_t attend(const mk_cache& c, int layer, const void* q, const int32_t* s
   p.tc_lanes = c.n_sm % w.tc_groups * 16 <= c.n_sm ? w.tc_groups : 1;  // where at most 1 SM of 16 is left without work
   p.tc_blocks = c.n_sm / p.tc_lanes;
   p.wide = p.group > 32;
-  p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * 1.44269504088896341f;
+  p.scale = (scale == 0.f ? 1.f / sqrtf((float)c.d.head_dim) : scale) * kLog2e;
   p.q = (const uint16_t*)q;
   p.seq_lens = seq_lens;
   p.out = (uint16_t*)out;

@@ -262,7 +262,7 @@ extern "C" int mk_cache_attend(mk_cache* c, int layer, const void* q, const int3
                                float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                                void* stream) {
   if (!c || !q || !seq_lens || !out || !workspace) return MK_ERR_INVALID_ARG;
-  if (layer < 0 || layer >= c->d.n_layers || prefix_len < 0 || prefix_len > c->d.max_ctx || !isfinite(scale) ||
+  if (layer < 0 || layer >= c->d.n_layers || prefix_len < 0 || prefix_len > c->d.max_ctx || !isfinite(scale * mk::kLog2e) ||
       workspace_bytes < mk::attend_workspace(c->d, c->n_sm))
     return MK_ERR_INVALID_ARG;
   if (!mk::aligned(q, 16) || !mk::aligned(out, 16) || !mk::aligned(seq_lens, 4) || !mk::aligned(lse, 4) ||

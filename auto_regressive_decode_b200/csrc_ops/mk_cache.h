@@ -14,6 +14,7 @@ namespace mk {
 constexpr int kCacheMaxBatch = 1024;  // sequences of a cache handle
 constexpr int kCacheMaxGroup = 64;    // query heads per KV head
 constexpr int kCachePageUnit = 16;    // page_size is a multiple of this
+constexpr float kLog2e = 1.44269504088896341f;  // scores are in units of log2
 constexpr int kWholeRows = 64;        // cache rows of a whole box of the tensor maps: an attention tile
 
 // What a kernel needs to find a row of the cache: contiguous

@@ -39,7 +39,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxTop = 32;
 constexpr int kVecs = 4;      // 16-byte vectors of logits a thread holds at once
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+constexpr float kLn2 = 0.693147180559945309f;
 typedef unsigned long long Key;
 
 struct ScoreParams {

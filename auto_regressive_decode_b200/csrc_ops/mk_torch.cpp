@@ -45,6 +45,14 @@ long integer(PyObject* o, const char* op, const char* name) {
   require(v >= INT_MIN && v <= INT_MAX, op, name, "out of range");
   return v;
 }
+double number(PyObject* o, const char* op, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    require(false, op, name, "a number is wanted");
+  }
+  return v;
+}
 bool on(const at::Tensor& t, int device) { return t.is_cuda() && t.get_device() == device; }
 const int32_t* ints(const at::Tensor& t, int64_t n, int device, const char* op, const char* name) {
   if (!t.defined()) return nullptr;
@@ -130,8 +138,8 @@ PyObject* do_attend(PyObject* const* a) {
   const int dev = c->device;
   const at::Tensor q = tensor(a[2], kOp, "q"), lens = tensor(a[3], kOp, "seq_lens");
   at::Tensor out = tensor(a[6], kOp, "out", true), lse = tensor(a[7], kOp, "lse", true), ws = tensor(a[8], kOp, "workspace", true);
-  const double scale = PyFloat_AsDouble(a[5]);
-  if (PyErr_Occurred()) return nullptr;
+  const double scale = number(a[5], kOp, "scale");
+  require(scale == 0 || (float)scale != 0.f, kOp, "scale", "0, or a number that is not 0 in fp32, is wanted");
   const int64_t shape[3] = {d.batch, d.n_q_heads, d.head_dim};
   auto whole = [&](const at::Tensor& t, int dims, at::ScalarType type, const char* name) {
     require(t.sizes() == at::IntArrayRef(shape, dims) && t.scalar_type() == type && on(t, dev) && t.is_contiguous(), kOp, name,

@@ -310,7 +310,8 @@ int mk_cache_append(mk_cache* c, int layer, const mk_append_args* args, void* st
  *   seq_lens  device int32[batch], each in [0, max_ctx]; a sequence of length 0
  *             gets zeros and lse -infinity, one shorter than the prefix attends
  *             its part of it
- *   scale     of the scores; 0: 1/sqrt(head_dim)
+ *   scale     of the scores; 0: 1/sqrt(head_dim).  Not so large that
+ *             scale * log2(e) is infinite
  *   out       device bf16 [batch][n_q_heads][head_dim]
  *   lse       device fp32 [batch][n_q_heads]: natural logarithm of the softmax
  *             sums, or NULL
