@@ -48,6 +48,9 @@ constexpr int kRegsFew = 64, kRegsMany = 104;
 static_assert(kRegsFew * 128 + kRegsMany * kSoftmaxThreads <= 96 * kTcThreads, "the launch's registers");
 constexpr int kHalf = kTcTile / 2;  // positions of a thread's half row
 constexpr float kSlack = 8.f;
+// References above it: a reference is a rounded product, and the exponent's fused product less the reference is then off
+// by more than 2^-4, without bound; product and difference are rounded one after the other instead.
+constexpr float kFar = 1 << 20;
 constexpr int kTcHead = 1;  // tiles that a group's start and end count as
 
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       q_phase ^= 1;
 
       float m = -INFINITY, l = 0.f;
+      bool far = false;  // of a row of the warp
       for (int i = 0; i < n; ++i) {
         const int t = a.pair ? i : 2 * i + s, t0 = (a.t0 + t) * kTcTile + c * kHalf;
         mbar_wait(smem_addr(&ctl->s_full[s]), s_phase, dead);
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? ex2(m - top) : 1.f;
           if (raise) m = top;
+          far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m) > kFar);
           l *= f;
           if (i > 0) {  // half of the stream's output so far: its last product was done before these scores
 #pragma unroll 1
@@ -411,7 +416,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        const F2 scale2 = pack2(scale, scale), back2 = pack2(-ref, -ref);
+        float by = scale, back = -ref;
+        if (far) {
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), scale), ref));
+          by = 1.f;
+          back = 0.f;
+        }
+        const F2 scale2 = pack2(by, by), back2 = pack2(back, back);
         F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
