@@ -683,6 +683,13 @@ extern "C" int mk_decode_greedy_scored(mk_handle* h, const mk_model_desc* desc, 
     return MK_ERR_INVALID_ARG;
   if (top_k > mk::kMaxTop) return MK_ERR_UNSUPPORTED;
   cudaStream_t s = (cudaStream_t)stream;
+  // a step's launch carries the step's number: replayed, its waits would find the counters of the steps before
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  if (capture != cudaStreamCaptureStatusNone) return MK_ERR_UNSUPPORTED;
   const int B = desc->batch;
   if (cudaMemcpyAsync(out_lens, seq_lens, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice, s) != cudaSuccess) {
     cudaGetLastError();

@@ -124,6 +124,8 @@ int mk_create(const mk_model_desc* desc, const mk_weights* weights, const mk_kv*
  *   out_logits device float[batch][vocab]
  * A device-side failure (range error, wait timeout) is reported by
  * mk_get_status; until then later steps return at once without computing.
+ * Not for stream capture, nor is mk_decode_greedy: each launch carries the
+ * number of its step, so that a replayed one does not wait for its parts.
  */
 int mk_decode_step(mk_handle* h, const int32_t* tokens, const int32_t* positions, const int32_t* seq_lens,
                    void* stream, float* out_logits);
@@ -226,7 +228,8 @@ int mk_decode_step_noalloc(const mk_model_desc* desc, const mk_weights* weights,
  * These entry points do the work around it: filling a cache with many rows,
  * attending for batches that share a long prefix, and scoring tokens.  They
  * follow the conventions above: asynchronous on `stream`, no allocation and no
- * host synchronisation after mk_cache_create, safe in stream capture.
+ * host synchronisation after mk_cache_create.  mk_cache_append,
+ * mk_cache_attend and mk_token_logprobs are safe in stream capture.
  *
  * A cache handle describes a cache (the same layouts as mk_kv; page_size is a
  * multiple of 16 here) and holds its rotation table and tensor maps.  It may
@@ -351,6 +354,8 @@ int mk_token_logprobs(const void* logits, int dtype, int64_t row_stride, int n_r
  * mk_decode_greedy with the scores of every picked token, mk_token_logprobs of
  * each step's logits.  `desc` is the one the handle was created with
  * (MK_ERR_INVALID_ARG where layers, batch, width or vocabulary differ).
+ * Refused within a stream capture (MK_ERR_UNSUPPORTED), as its steps are not
+ * for replaying.
  *   out_lens   device int32[batch]: the lengths after the loop (also its
  *              working state; not the array seq_lens)
  *   logits     device fp32[batch][vocab]: the last step's logits afterwards

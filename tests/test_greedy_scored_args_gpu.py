@@ -74,3 +74,24 @@ def test_larger_buffers_and_a_stream_of_its_own():
     st.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(a, b) and (a[3:] == -5).all() and all(torch.equal(x, y) for x, y in zip(first, second))
+
+
+def test_refused_within_a_capture():
+    """The steps carry their numbers, so that a replay would be wrong; the capture goes on without the call."""
+    import auto_regressive_decode_b200.mk as mk
+    cfg, dec, tok, lens = decoder()
+    picks = torch.full((2, cfg.batch), -5, dtype=torch.int32, device="cuda")
+    x = torch.zeros(3, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        with pytest.raises(mk.MkError) as e:
+            dec.greedy_scored(2, tok, lens, picks)
+        x.add_(1)
+    assert e.value.code == mk.MK_ERR_UNSUPPORTED
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (x == 2).all() and (picks == -5).all()
+    dec.greedy_scored(2, tok, lens, picks)
+    assert dec.status() == mk.MK_OK and (picks >= 0).all()
