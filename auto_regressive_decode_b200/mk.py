@@ -444,7 +444,8 @@ class Cache:
                stream=None):
         """Append keys and values (bf16 or fp32 [n][n_kv][hd]) to the cache, the keys rotated; returns the rotated
         q (bf16 [n][n_q][hd]) where q is given.  seq_lens int32 [B]: rows held before; starts int32 [B + 1]: the
-        tokens of each sequence (None: one each); see mk_cache_append."""
+        tokens of each sequence (None: one each); see mk_cache_append.  Rows of q of tokens that belong to no sequence are
+        left as they were in q_out, and hold anything without it."""
         if stream is not None:
             with _on_stream(stream, self.device):
                 return self._call.append(self.h, layer, k, v, seq_lens, q, starts, positions, q_norm, k_norm, q_out)

@@ -287,9 +287,11 @@ enum { MK_DTYPE_BF16 = 0, MK_DTYPE_FP32 = 1 };
  *   q_norm, k_norm device bf16[head_dim] or NULL: RMSNorm (rms_eps) of each
  *             query / key head with this gain before the rotation
  *   q_out     device bf16 [n_tokens][n_q_heads][head_dim], with q
- * Arithmetic is fp32; each result is rounded once, to bf16.  A token whose row
- * is outside [0, max_ctx), whose page is outside the pool or whose position is
- * out of range is not written (MK_ERR_RANGE).  No two tokens of a call share a
+ * Arithmetic is fp32 (a norm's reciprocal root is within 2^-22 of its value);
+ * each result is rounded once, to bf16.  A token whose row is outside
+ * [0, max_ctx), whose page is outside the pool or whose position is out of
+ * range is not written (MK_ERR_RANGE).  The rows of q_out of tokens that are
+ * left out or not written stay as they were.  No two tokens of a call share a
  * row unless the block table maps two sequences' new rows to one page.
  */
 typedef struct mk_append_args {
