@@ -5,8 +5,8 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain
 //   out[i]     = y[i] cos a_i - y[i + hd/2] sin a_i
 //   out[i + h] = y[i + hd/2] cos a_i + y[i] sin a_i,   a_i = pos theta^(-2i/hd)
-// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 232 us, 6.5
-// TB/s; 4100 of 48 bf16 rows 21.5 us, 4.7 TB/s (the latency of finding a token's place; 17.7 with the
+// Bound: memory (3 flops a value): 16384 tokens of 120 fp32 rows of 128 (1.5 GB) take 232 to 236 us, 6.4
+// to 6.5 TB/s; 4100 of 48 bf16 rows 19.6 us, 5.1 TB/s (the latency of finding a token's place; 18.5 with the
 // rows in the L2 cache); one token of each of 8 sequences 2.1 us, a launch.
 // hd/16 neighbouring lanes hold a row, each 8 values of its first half and the 8
 // they pair with, so that loads and stores are 16 bytes and a lane's cos/sin (8

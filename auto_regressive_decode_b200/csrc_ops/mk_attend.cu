@@ -21,7 +21,7 @@
 // Measured with the join, heads of 128: 32 sequences of 4000 to 4096 positions, 8 KV heads,
 // 87 us, 6.1 TB/s; 8 sequences of 40 heads over 2048 shared and up to 2048 own positions
 // 42 us, 5.2 TB/s; 512 sequences of 64 positions 42 us, 3.4 TB/s (starting and ending a
-// piece takes 2600 of its 5500 clocks); one sequence over 1024 7.4 us, two launches' latency.
+// piece takes 2600 of its 5000 clocks); one sequence over 1024 7.4 us, two launches' latency.
 //
 // Up to 8 rows (NARROW) are the N of the products, S^T = K Q^T and O^T = V^T P^T;
 // more are their M, 16 at a time.  As M, 8 rows would take twice the products and
@@ -43,7 +43,7 @@ constexpr int kAttThreads = kComputeThreads + 32;
 constexpr int kHead = 2;                         // tiles that a group's start and end count as
 // Rows of a KV head that share a prefix: more go to the tensor-core kernel, which does 128 in the time of one.
 // 32 rows over 2500 positions (8 KV heads) take 16.5 us here and 18.4 there, 64 rows 21.0 and 20.3; over 16000 27.5 and
-// 26.4, 39.9 and 28.3.
+// 26.4, 39.9 and 28.3 (by rows alone; the length would move the limit a little).
 constexpr int kTcFrom = 32;
 
 template <int HD, bool NARROW>

@@ -28,9 +28,9 @@
 // Bound: the tensor cores (4 head_dim flops a row and position) and, nearly as
 // much, the exponentials (16 a clock and SM: 128 x 128 of them last as long as the
 // tile's two products); with up to about 128 rows, the cache's bytes.  1024 rows of 8
-// KV heads over 65536 positions: 235 us with the join, 1170 TFLOP/s; 128 rows: 62 us,
+// KV heads over 65536 positions: 235 to 255 us with the join (by the machine), 1080 to 1170 TFLOP/s; 128 rows: 62 us,
 // 4.3 TB/s.  A stream's products and softmax alternate, about 1300 and 2000 clocks a
-// tile of 128 x 128; a third stream has no room in tensor memory.
+// tile of 128 x 128; for heads of 128 a third stream has no room in tensor memory.
 #include <type_traits>
 
 #include "mk_attend.h"

@@ -14,12 +14,12 @@
 // the thread groups' maxima is a limit that k keys reach; the few chunk shares that
 // reach it are read once more and their keys ranked.  (Candidates collected on the
 // way, against a limit raised after chunks 1, 2, 4, ..., cost two barriers a raise and the slower
-// the later the best ones came: 137 us for the 2047 rows below, 310 for 444 ascending ones, now 38.)
+// the later the best ones came: 137 us instead of 117 for the 2047 rows below, 310 instead of 38 for 444 ascending ones.)
 // The result does not depend on the order of arrival.
 //
 // Bound: memory for many rows (one read of the logits), at half of the issue slots and of the
-// exponentials' rate: 2047 rows of 128256 bf16 logits take 96 us without alternatives (5.5
-// TB/s) and 117 with 20 (4.5 TB/s); short rows, the latency of a row's join: 2000 of 32000 bf16 35 and 53 us.
+// exponentials' rate: 2047 rows of 128256 bf16 logits take 88 us without alternatives (5.9
+// TB/s) and 104 with 20 (5.1 TB/s); short rows, the latency of a row's join: 2000 of 32000 bf16 29 and 44 us.
 // Few rows: each is cut over the blocks of a cluster, which join through distributed
 // shared memory: no workspace, one launch.
 #include <cooperative_groups.h>
@@ -628,11 +628,11 @@ cudaError_t launch(const ScoreParams& p, int parts, int n_sm, cudaStream_t strea
 template <typename T>
 cudaError_t score(const ScoreParams& p, int n_sm, cudaStream_t stream) {
   // More rows than large blocks fit the SMs, and not long: small blocks, twice as many (20 alternatives of bf16
-  // rows: 500 of 4096 8.5 us against 13.2, 2000 of 16000 34 against 37, of 32000 53 against 52, of 50257 72 against 74;
-  // 200 of 32000 13.0 against 10.7).
+  // rows: 500 of 4096 7.4 us against 11.6, 2000 of 16000 30.5 against 33.7, of 32000 43.7 against 44.6, 1000 of 32000 24.7
+  // against 24.1, 200 of 32000 11.6 against 9.9; of fp32 rows of 50257 79 both; 2000 bf16 rows of 50257 would gain, 58 against 62).
   if (p.rows > 3 * n_sm && p.vocab <= 32768) return launch<T, 128>(p, 1, n_sm, stream);
   // Few rows: as many blocks a row as fill the SMs, 4096 logits a block at least (20 alternatives of fp32 rows: one of
-  // 128256 9.5 us, 18.0 as one block; 64 of 151936 14.6 with 4 blocks each, 22.5 with one, 25.6 with 8).
+  // 128256 9.1 us, 15.9 as one block; 64 of 151936 13.8 with 4 blocks each, 19.3 with one, 21.3 with 8).
   int parts = 1;
   while (parts < kMaxParts && p.rows * parts < n_sm && p.vocab / (2 * parts) >= 4096) parts *= 2;
   return launch<T, 256>(p, parts, n_sm, stream);
